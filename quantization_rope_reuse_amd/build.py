@@ -24,7 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhkv.so")
 SOURCES = ("api.hip", "quant.hip", "fetch.hip", "crc.hip", "order.hip", "streams.hip",
            "select.hip", "frames.hip", "probe.hip", "noalloc.hip",
-           "staged.hip")
+           "staged.hip", "serve_api.hip", "plan.hip", "rope.hip", "append.hip", "attend.hip")
 ARCH = "gfx950"
 
 

@@ -236,6 +236,14 @@ bool span_ok(std::initializer_list<Extent> dims, int64_t tail) {
   return true;
 }
 
+int element_size(int32_t dtype) { return elem_size(dtype); }
+
+int shape_check(const hkv_shape* shape, Geometry* g) { return check_shape(shape, g); }
+
+int records_check(const hkv_records* r, int32_t fmt, const hkv_shape* shape, RecordView* v) {
+  return check_records(r, fmt, shape, v);
+}
+
 int fetch_check(const hkv_shape* shape, int32_t fmt, const hkv_records* src,
                 const int32_t* block_table, const int32_t* delta_m, double rope_base,
                 int32_t pairs, const hkv_pages* dst, int32_t dst_dtype, FetchViews* f) {

@@ -69,6 +69,13 @@ struct Extent {
 };
 bool span_ok(std::initializer_list<Extent> dims, int64_t tail);
 
+// Checks shared by the C entry points: a dtype's element size (0 if it is
+// none), the launch geometry of a shape, and a records view (which refuses
+// an unknown format).
+int element_size(int32_t dtype);
+int shape_check(const hkv_shape* shape, Geometry* g);
+int records_check(const hkv_records* r, int32_t fmt, const hkv_shape* shape, RecordView* v);
+
 // Validated views of one fetch call (hkv_fetch_dequant_rope_shift's checks).
 struct FetchViews {
   Geometry g;

@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libhkv (include/hkv.h).
+"""Thin ctypes binding of libhkv (include/hkv.h, include/hkv_serve.h).
 
 Argument marshalling only: every step of put, CRC and fetch runs in the HIP
 kernels of libhkv.so.  torch is used for device memory and streams: tensors
@@ -11,6 +11,7 @@ the library raises.
 
 from __future__ import annotations
 
+import collections
 import ctypes
 import functools
 import os
@@ -61,6 +62,43 @@ class Records(ctypes.Structure):
 class HostRecords(ctypes.Structure):
     _fields_ = [("host_base", ctypes.c_void_p), ("layer_stride_bytes", ctypes.c_int64),
                 ("block_stride_bytes", ctypes.c_int64)]
+
+
+# Structures of include/hkv_serve.h.
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
+
+
+class Step(ctypes.Structure):
+    _fields_ = [("n_requests", ctypes.c_int32), ("block_tokens", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("kv_len", ctypes.c_void_p), ("new_tokens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("free_blocks", ctypes.c_void_p), ("free_capacity", ctypes.c_int32),
+                ("free_count", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p),
+                ("kv_len_out", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("refused", ctypes.c_void_p)]
+
+
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("pairs", ctypes.c_int32),
+                ("rope_base", ctypes.c_double), ("axis", ctypes.c_int8 * (HEAD_DIM // 2)),
+                ("freq", ctypes.c_uint8 * (HEAD_DIM // 2))]
+
+
+class Requests(ctypes.Structure):
+    _fields_ = [("n_requests", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("max_queries", ctypes.c_int32), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p)]
+
+
+class KeyShift(ctypes.Structure):
+    _fields_ = [("delta_m", ctypes.c_void_p), ("rope_base", ctypes.c_double),
+                ("pairs", ctypes.c_int32)]
 
 
 _lib = None
@@ -141,6 +179,22 @@ def lib():
                      "hkv_crc32_blocks",
                      "hkv_page_visit_order", "hkv_token_drift", "hkv_select_top_tokens",
                      "hkv_frame_headers", "hkv_frame_verify", "hkv_frame_delta_m"):
+            getattr(l, name).restype = ctypes.c_int
+        l.hkv_plan_step.argtypes = [P(Step), vp]
+        l.hkv_rope_heads.argtypes = [P(RopeAxes), vp, ctypes.c_int64, ctypes.c_int32, P(Heads),
+                                     P(Heads), P(Heads), P(Heads), ctypes.c_int32,
+                                     ctypes.c_int32, vp]
+        l.hkv_append_tokens.argtypes = [P(Shape), ctypes.c_int32, P(Heads), P(Heads),
+                                        ctypes.c_int32, ctypes.c_int32, vp, P(Records), vp]
+        l.hkv_attend_records.argtypes = [
+            P(Shape), ctypes.c_int32, P(Records), P(Requests), P(Heads), ctypes.c_int32,
+            ctypes.c_int32, ctypes.c_double, ctypes.c_int32, P(KeyShift), P(Heads), vp, vp,
+            ctypes.c_int64, vp]
+        l.hkv_attend_workspace_bytes.argtypes = [P(Shape), P(Requests), ctypes.c_int32,
+                                                 ctypes.c_int32, ctypes.c_int32]
+        l.hkv_attend_workspace_bytes.restype = ctypes.c_int64
+        for name in ("hkv_plan_step", "hkv_rope_heads", "hkv_append_tokens",
+                     "hkv_attend_records"):
             getattr(l, name).restype = ctypes.c_int
         l.hkv_record_bytes.argtypes = [ctypes.c_int32] * 4
         l.hkv_record_bytes.restype = ctypes.c_int64
@@ -683,3 +737,255 @@ def stream_probe_put(src, dst, stream=None):
         ctypes.c_void_p(src.data_ptr()), ctypes.c_void_p(dst.data_ptr()), dst.numel(),
         _stream(stream, src.device)))
     return dst
+
+
+# ---------------------------------------------------------------------------
+# Serving from records (include/hkv_serve.h)
+# ---------------------------------------------------------------------------
+
+StepPlan = collections.namedtuple("StepPlan", ["kv_len", "q_start", "positions", "slots",
+                                               "refused", "free_count"])
+
+
+def alloc_plan(n_requests: int, n_tokens: int, device="cuda") -> StepPlan:
+    """Output tensors of plan_step for n_requests requests and up to n_tokens
+    new tokens."""
+    def i32(n):
+        return torch.empty(n, dtype=torch.int32, device=device)
+    return StepPlan(i32(n_requests), i32(n_requests + 1), i32(n_tokens),
+                    torch.empty(n_tokens, dtype=torch.int64, device=device), i32(n_requests),
+                    i32(1))
+
+
+def _table(t: torch.Tensor):
+    """Entries per row and row stride of an int32 [n_requests, max_blocks]
+    tensor; strides that address nothing may be anything."""
+    if t.dim() != 2 or t.dtype != torch.int32 or (
+            t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("block_table must be an int32 [n_requests, max_blocks] tensor, last "
+                         "axis contiguous")
+    return t.shape[1], t.stride(0) if t.shape[0] > 1 and t.numel() > 0 else t.shape[1]
+
+
+@_on_one_gpu
+def _plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, out_kv_len, q_start,
+               positions, slots, refused, out_count, block_tokens, stream):
+    R = kv_len.numel()
+    mb, stride = _table(block_table)
+    if block_table.shape[0] != R or new_tokens.numel() != R or out_kv_len.numel() != R \
+            or refused.numel() != R or q_start.numel() != R + 1:
+        raise ValueError("kv_len, new_tokens, block_table, refused [n_requests] and q_start "
+                         "[n_requests + 1] must agree")
+    if free_count.numel() != 1 or out_count.numel() != 1:
+        raise ValueError("free_count must hold one element")
+    if slots.dtype != torch.int64 or not slots.is_contiguous() or \
+            slots.numel() != positions.numel():
+        raise ValueError("slots must be a contiguous int64 tensor as long as positions")
+    step = Step(R, int(block_tokens), mb, positions.numel(), _i32(kv_len, "kv_len"),
+                _i32(new_tokens, "new_tokens"), block_table.data_ptr(), stride,
+                _i32(free_blocks, "free_blocks"), free_blocks.numel(),
+                _i32(free_count, "free_count"), _i32(out_count, "free_count"),
+                _i32(out_kv_len, "kv_len"), _i32(q_start, "q_start"),
+                _i32(positions, "positions"), ctypes.c_void_p(slots.data_ptr()),
+                _i32(refused, "refused"))
+    _check("hkv_plan_step", lib().hkv_plan_step(ctypes.byref(step),
+                                                _stream(stream, kv_len.device)))
+
+
+def plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, block_tokens: int,
+              n_tokens: int, out=None, stream=None) -> StepPlan:
+    """The plan of one step from its request lengths: table entries for the
+    blocks that new tokens need (written into block_table, taken from the
+    stack free_blocks[:free_count]), new lengths, packed query starts,
+    positions and slots of up to n_tokens tokens.  new_tokens[r] < 0 ends
+    request r and returns its blocks.  A request that does not fit is marked
+    in refused and keeps its length.  kv_len, new_tokens, free_count: int32
+    on the GPU; free_count of the result is the next step's.  out: a StepPlan
+    of tensors to write (alloc_plan), none of them an input."""
+    if out is None:
+        out = alloc_plan(kv_len.numel(), int(n_tokens), device=kv_len.device)
+    if out.positions.numel() != n_tokens:
+        raise ValueError("out must hold n_tokens positions")
+    _plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, *out[:5],
+               out.free_count, block_tokens, stream)
+    return out
+
+
+def _heads(t: torch.Tensor, name: str):
+    """[n_tokens, n_heads, 128] rows of head vectors."""
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a [n_tokens, n_heads, {HEAD_DIM}] tensor, last axis "
+                         "contiguous")
+    if t.dtype not in TORCH_DTYPES:
+        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+    # the stride of an axis of one entry addresses nothing and may be anything
+    return Heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0,
+                 t.stride(1) if t.shape[1] > 1 else 0, t.shape[1])
+
+
+@functools.lru_cache(maxsize=64)
+def rope_axes(rope_base: float, pairs, sections=(HEAD_DIM // 2,), order="blocked", freq=None):
+    """The axes of rope_heads.  sections: pairs per axis, at most 64 in all;
+    the rest do not turn.  order: "blocked" gives each axis a run of pairs,
+    "interleaved" lets the axes take turns (one pair each, those with pairs
+    left going on), or a tuple of 64 axis numbers (-1: does not turn; sections
+    is then ignored).  freq: each pair's frequency index (default: its own)."""
+    half = HEAD_DIM // 2
+    if isinstance(order, str):
+        sections = tuple(int(s) for s in sections)
+        if order not in ("blocked", "interleaved") or min(sections) < 0 or sum(sections) > half:
+            raise ValueError("sections must be counts of at most 64 pairs in all, order "
+                             "'blocked' or 'interleaved'")
+        if order == "blocked":
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        else:
+            axis = [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+        axis += [-1] * (half - len(axis))
+        n_axes = len(sections)
+    else:
+        axis = [int(a) for a in order]
+        n_axes = max(max(axis) + 1, 1)
+    freq = list(range(half)) if freq is None else [int(f) for f in freq]
+    if len(axis) != half or len(freq) != half or not all(-1 <= a < n_axes for a in axis) \
+            or not all(0 <= f < HEAD_DIM for f in freq):
+        raise ValueError("64 axis numbers and 64 frequency indexes (0..127) are needed")
+    return RopeAxes(n_axes, PAIRS[pairs], float(rope_base),
+                    (ctypes.c_int8 * half)(*axis), (ctypes.c_uint8 * half)(*freq))
+
+
+@_on_one_gpu
+def rope_heads(q, k, positions, rope_base: float, pairs, sections=(HEAD_DIM // 2,),
+               order="blocked", freq=None, inverse: bool = False, q_out=None, k_out=None,
+               stream=None):
+    """Rotary positions for query and key heads, [n_tokens, n_heads, 128] each
+    (k may be None).  positions: int32 [n_tokens], or [n_axes, n_tokens] for
+    positions with several axes (see rope_axes for sections, order and freq).
+    inverse=True turns back: it strips positions, and it is the gradient with
+    respect to q and k given that of the results.  q_out, k_out: tensors to
+    write, the inputs themselves for a rotation in place."""
+    axes = rope_axes(float(rope_base), pairs, tuple(sections),
+                     order if isinstance(order, str) else tuple(order),
+                     None if freq is None else tuple(freq))
+    n = q.shape[0]
+    pos = positions if positions.dim() == 2 else positions.unsqueeze(0)
+    if pos.dim() != 2 or pos.dtype != torch.int32 or pos.shape != (axes.n_axes, n) or (
+            n > 1 and pos.stride(1) != 1):
+        raise ValueError(f"positions must be int32 [{axes.n_axes}, n_tokens], last axis contiguous")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    heads = [_heads(q, "q"), Heads(), _heads(q_out, "q_out"), Heads()]
+    same = q_out.shape == q.shape and q_out.dtype == q.dtype
+    if k is not None:
+        heads[1], heads[3] = _heads(k, "k"), _heads(k_out, "k_out")
+        same = same and k.shape[0] == n and k_out.shape == k.shape and \
+            k.dtype == k_out.dtype == q.dtype
+    if not same:
+        raise ValueError("q, k and their outputs must share dtype and n_tokens, each output its "
+                         "input's shape")
+    st = lib().hkv_rope_heads(ctypes.byref(axes), ctypes.c_void_p(pos.data_ptr()),
+                              pos.stride(0) if axes.n_axes > 1 else 0, n,
+                              *(ctypes.byref(h) for h in heads), TORCH_DTYPES[q.dtype],
+                              1 if inverse else 0, _stream(stream, q.device))
+    _check("hkv_rope_heads", st)
+    return q_out, k_out
+
+
+def _pool(records, fmt, block_tokens, n_kv_heads):
+    """One layer's records [n_blocks, bytes] (or [1, n_blocks, bytes])."""
+    r = records if records.dim() == 3 else records.unsqueeze(0)
+    if r.dim() != 3 or r.shape[0] != 1:
+        raise ValueError("records must be one layer's uint8 [n_blocks, bytes] tensor")
+    return (Shape(1, r.shape[1], block_tokens, n_kv_heads, HEAD_DIM),
+            _records(r, fmt, block_tokens, n_kv_heads))
+
+
+@_on_one_gpu
+def append_tokens(k, v, slots, records, fmt, block_tokens: int, stream=None):
+    """Quantize the new tokens' keys and values, [n_tokens, n_kv_heads, 128]
+    each, into slots (int64 [n_tokens]; block * block_tokens + token, negative
+    to skip) of one layer's records [n_blocks, bytes]."""
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must share shape and dtype")
+    kh, vh = _heads(k, "k"), _heads(v, "v")
+    if slots.dtype != torch.int64 or not slots.is_contiguous() or slots.numel() != k.shape[0]:
+        raise ValueError("slots must be a contiguous int64 tensor of n_tokens elements")
+    shape, rec = _pool(records, fmt, block_tokens, k.shape[1])
+    st = lib().hkv_append_tokens(ctypes.byref(shape), FORMATS[fmt], ctypes.byref(kh),
+                                 ctypes.byref(vh), TORCH_DTYPES[k.dtype], k.shape[0],
+                                 ctypes.c_void_p(slots.data_ptr()), ctypes.byref(rec),
+                                 _stream(stream, k.device))
+    _check("hkv_append_tokens", st)
+    return records
+
+
+def attend_workspace_bytes(n_blocks: int, block_tokens: int, n_kv_heads: int, n_requests: int,
+                           max_blocks: int, n_tokens: int, n_q_heads: int, max_queries: int,
+                           dtype) -> int:
+    shape = Shape(1, n_blocks, block_tokens, n_kv_heads, HEAD_DIM)
+    req = Requests(n_requests, max_blocks, max_queries, None, max_blocks, None, None)
+    return int(lib().hkv_attend_workspace_bytes(ctypes.byref(shape), ctypes.byref(req), n_tokens,
+                                                n_q_heads, TORCH_DTYPES[dtype]))
+
+
+@_on_one_gpu
+def attend_records(q, records, fmt, block_tokens: int, n_kv_heads: int, block_table, kv_len,
+                   q_start=None, max_queries=None, sm_scale=None, causal: bool = True,
+                   delta_m=None, rope_base: float = 10000.0, pairs="half_split", out=None,
+                   lse=None, workspace=True, stream=None):
+    """Attention of q [n_tokens, n_q_heads, 128] over one layer's records
+    [n_blocks, bytes]; returns (out, lse), lse float32 [n_tokens, n_q_heads].
+    block_table int32 [n_requests, max_blocks], kv_len int32 [n_requests] with
+    the step's own tokens counted, q_start int32 [n_requests + 1] (None: one
+    query per request), max_queries the most queries of a request (default
+    n_tokens; a smaller true bound saves empty work).  sm_scale: 1 / sqrt(128)
+    if None.  causal: query j of n sees tokens up to kv_len - n + j.  delta_m:
+    int32 [n_requests, max_blocks], moves the stored keys of each table entry
+    as fetch_dequant_rope_shift does (rope_base, pairs).  workspace: True
+    (allocated here if one is needed), or a uint8 tensor of
+    attend_workspace_bytes bytes."""
+    heads = _heads(q, "q")
+    n, hq = q.shape[0], q.shape[1]
+    mb, stride = _table(block_table)
+    R = block_table.shape[0]
+    if kv_len.numel() != R or (q_start is not None and q_start.numel() != R + 1) or \
+            (q_start is None and n != R):
+        raise ValueError("kv_len [n_requests], q_start [n_requests + 1] (or one query per "
+                         "request) and block_table must agree")
+    if max_queries is None:
+        max_queries = 1 if q_start is None else max(n, 1)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if lse is None:
+        lse = torch.empty((n, hq), dtype=torch.float32, device=q.device)
+    if lse.shape != (n, hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [n_tokens, n_q_heads] tensor")
+    shift = None
+    if delta_m is not None:
+        if delta_m.shape != block_table.shape or _table(delta_m) != (mb, stride):
+            raise ValueError("delta_m must have block_table's shape, type and strides")
+        shift = ctypes.byref(KeyShift(delta_m.data_ptr(), float(rope_base), PAIRS[pairs]))
+    shape, rec = _pool(records, fmt, block_tokens, n_kv_heads)
+    req = Requests(R, mb, int(max_queries), block_table.data_ptr(), stride,
+                   _i32(kv_len, "kv_len"), None if q_start is None else _i32(q_start, "q_start"))
+    need = lib().hkv_attend_workspace_bytes(ctypes.byref(shape), ctypes.byref(req), n, hq,
+                                            TORCH_DTYPES[q.dtype])
+    if workspace is True:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        ws_ptr, ws_bytes = ctypes.c_void_p(workspace.data_ptr()), workspace.numel()
+    oh = _heads(out, "out")
+    st = lib().hkv_attend_records(
+        ctypes.byref(shape), FORMATS[fmt], ctypes.byref(rec), ctypes.byref(req),
+        ctypes.byref(heads), TORCH_DTYPES[q.dtype], n,
+        float(HEAD_DIM ** -0.5 if sm_scale is None else sm_scale), 1 if causal else 0, shift,
+        ctypes.byref(oh), ctypes.c_void_p(lse.data_ptr()), ws_ptr, ws_bytes,
+        _stream(stream, q.device))
+    _check("hkv_attend_records", st)
+    return out, lse
