@@ -24,7 +24,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhkv.so")
 SOURCES = ("api.hip", "quant.hip", "fetch.hip", "crc.hip", "order.hip", "streams.hip",
            "select.hip", "frames.hip", "probe.hip", "noalloc.hip",
-           "staged.hip", "serve_api.hip", "plan.hip", "rope.hip", "append.hip", "attend.hip")
+           "staged.hip", "serve_api.hip", "plan.hip", "rope.hip", "append.hip", "attend.hip",
+           "attend_rows_int4.hip", "attend_rows_fp8.hip")
 ARCH = "gfx950"
 
 
@@ -65,7 +66,7 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
         jobs.append([cc, *compile_flags(), "-c", os.path.join(CSRC, src), "-o", obj])
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(4, len(jobs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         for f in [ex.submit(_run, j, verbose) for j in jobs]:
             f.result()
     tmp = LIB + ".tmp"

@@ -1,189 +1,148 @@
-// Attention of queries over compressed records.
-//
-// One wave per (query row, query head), 8 lanes per cached vector, 8 tokens
-// a step: each group of 8 lanes forms its token's score from the codes
-// (scale and sm_scale applied in fp32), keeps its own running maximum, sum
-// and weighted values, and the 8 groups are joined at the end.  Keys that
-// moved by delta are met by the query turned by -delta: q . R(delta) k =
-// R(-delta) q . k.
-#include "rope_device.h"
-#include "serve_launch.h"
+// Attention of queries over compressed records: how the work is shared out,
+// and the join of partial results.
+#include "attend_rows.h"
 
 namespace hkv {
 namespace {
 
-struct AttendParams {
-  const uint8_t* rec;
-  int64_t rec_block;
-  int32_t n_blocks, block_tokens, n_heads, vecs;
-  const int32_t* table;
-  int64_t table_stride;
-  const int32_t* kv_len;
-  const int32_t* q_start;
-  int32_t max_len;
-  int32_t max_queries;
-  int32_t n_tokens;
-  const char* q;
-  char* out;
-  int64_t q_token, q_head, o_token, o_head;
-  int32_t q_heads, group;
-  float* lse;
-  float scale_log2;        // sm_scale * log2(e)
-  int32_t causal;
-  const int32_t* delta;
-  double theta[kHeadDim / 2];
+// One workgroup per row that more than one range worked on: each wave takes
+// every fourth partial result, a lane two dims; then the waves join in order.
+constexpr int kJoinWaves = 4;
+
+__global__ __launch_bounds__(kJoinWaves * kWave) void attend_join_kernel(AttendParams p, int item_rows) {
+  const int r = blockIdx.y;
+  const Span s = span_of(p, r);
+  const int j = blockIdx.x / p.q_heads;
+  if (j >= min(s.n_q, p.max_queries)) return;
+  const int head = blockIdx.x - j * p.q_heads;
+  const int kh = head / p.group;
+  const int row = j * p.group + (head - kh * p.group);
+  const int item = row / item_rows;
+  const uint64_t tiles = tiles_of(s);
+  const uint64_t f0 = p.prefix_out[r] + item * tiles;
+  const uint64_t per = p.prefix_out[p.n_requests + 1];
+  const int64_t w0 = f0 / per, w1 = (f0 + tiles - 1) / per;
+  if (w0 == w1) return;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = threadIdx.x / kWave;
+  const int64_t in_item = row - item * item_rows;
+  auto at = [&](int64_t w) {
+    const int64_t which = w == w0 && f0 > static_cast<uint64_t>(w0) * per ? 1 : 0;
+    return ((w * 2 + which) * p.n_heads + kh) * p.part_rows + in_item;
+  };
+  float m = kNoReference, l = 0.0f;
+  float2 o = make_float2(0.0f, 0.0f);
+  constexpr int kBatch = 8;
+  for (int64_t w = w0 + wave; w <= w1; w += kJoinWaves * kBatch) {
+    float2 ml[kBatch], x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = at(min(w + u * kJoinWaves, w1));
+      ml[u] = reinterpret_cast<const float2*>(p.part_ml)[i];
+      x[u] = reinterpret_cast<const float2*>(p.part_o + i * kHeadDim)[lane];
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (w + u * kJoinWaves <= w1) top = fmaxf(top, ml[u].x);
+    const float keep = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+    l *= keep;
+    o.x *= keep;
+    o.y *= keep;
+    m = top;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (w + u * kJoinWaves > w1) break;
+      const float f = ml[u].x == m ? 1.0f : __builtin_amdgcn_exp2f(ml[u].x - m);
+      l += ml[u].y * f;
+      o.x += x[u].x * f;
+      o.y += x[u].y * f;
+    }
+  }
+  __shared__ float2 join_ml[kJoinWaves];
+  __shared__ float2 join_o[kJoinWaves][kWave];
+  join_o[wave][lane] = o;
+  if (lane == 0) join_ml[wave] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x >= kHeadDim / 8) return;     // 8 dims a lane
+  float top = kNoReference, sum = 0.0f, y[8] = {};
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) top = fmaxf(top, join_ml[w].x);
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) {
+    const float f = join_ml[w].x == top ? 1.0f : __builtin_amdgcn_exp2f(join_ml[w].x - top);
+    sum += join_ml[w].y * f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = join_o[w][4 * threadIdx.x + i];
+      y[2 * i] += a.x * f;
+      y[2 * i + 1] += a.y * f;
+    }
+  }
+  const bool empty = sum == 0.0f;
+  const float inv = empty ? 0.0f : 1.0f / (sum * kWeightScale);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = empty ? 0.0f : y[i] * inv;
+  const int64_t query = s.start + j;
+  store8_any(p.dtype, p.out + query * p.o_token + head * p.o_head + 8 * threadIdx.x * p.elem, y);
+  if (p.lse && threadIdx.x == 0)
+    p.lse[query * p.q_heads + head] = log_sum(top, sum);
+}
+
+struct Share {
+  int nt;                  // 16 nt rows per item
+  int set_heads, head_sets, ranges, min_tiles, part_rows;
+  int64_t rows;            // partial rows in all
+  int64_t items;           // of one request, at most
 };
 
-template <int FMT>
-__device__ __forceinline__ void load_vector(const uint8_t* codes, int64_t v, int sub,
-                                            float (&a)[8], float (&b)[8]) {
-  if constexpr (FMT == kFP8) {
-    const uint8_t* c = codes + v * kHeadDim + 8 * sub;
-    fp8x8_to_f32(*reinterpret_cast<const u32x2*>(c), a);
-    fp8x8_to_f32(*reinterpret_cast<const u32x2*>(c + 64), b);
-  } else {
-    const uint8_t* c = codes + v * (kHeadDim / 2) + 4 * sub;
-    int4x8_to_f32(*reinterpret_cast<const uint32_t*>(c), a);
-    int4x8_to_f32(*reinterpret_cast<const uint32_t*>(c + 32), b);
+// How a call's work is shared out, from the sizes that the host knows.
+Share share_of(int fmt, const Geometry& g, const hkv_requests& req, int32_t n_tokens,
+               int32_t n_q_heads, int dtype) {
+  Share s;
+  const int64_t queries = req.max_queries < n_tokens ? req.max_queries : n_tokens;
+  const int64_t rows = queries * (n_q_heads / g.n_heads);
+  s.nt = dtype == kF32 || rows <= 16 ? 1 : 2;
+  const int64_t item_rows = 16 * s.nt;
+  s.items = (rows + item_rows - 1) / item_rows;
+  const int64_t max_len = static_cast<int64_t>(req.max_blocks) * g.block_tokens;
+  const int64_t tiles = max_len < kTileTokens ? 1 : (max_len + kTileTokens - 1) / kTileTokens;
+  // Two INT4 heads of a token share a 128-byte line, so one workgroup reads both.
+  s.set_heads = fmt == kINT4 && g.n_heads % 2 == 0 ? 2 : 1;
+  s.head_sets = g.n_heads / s.set_heads;
+  const int64_t phases = kRowsWaves / s.set_heads;
+  s.ranges = 0;
+  s.min_tiles = static_cast<int>(2 * phases);
+  s.part_rows = static_cast<int>(rows < item_rows ? rows : item_rows);
+  if (req.n_requests <= kMaxFlatRequests && tiles > 4 * phases && queries * n_q_heads <= (1 << 20)) {
+    const int64_t all = static_cast<int64_t>(req.n_requests) * s.items * tiles;
+    int64_t ranges = 512 / s.head_sets;
+    const int64_t most = (all + s.min_tiles - 1) / s.min_tiles;
+    ranges = ranges < 1 ? 1 : ranges;
+    s.ranges = static_cast<int>(ranges < most ? ranges : most);
   }
+  s.rows = static_cast<int64_t>(s.ranges) * 2 * g.n_heads * s.part_rows;
+  return s;
 }
 
-template <int FMT, int DT, int PAIRS>
-__global__ __launch_bounds__(kWave) void attend_kernel(AttendParams p) {
-  constexpr int CB = FMT == kFP8 ? kHeadDim : kHeadDim / 2;
-  constexpr int ES = ElemSize<DT>::value;
-  const int lane = threadIdx.x;
-  const int sub = lane & (kLanesPerVec - 1);
-  const int grp = lane / kLanesPerVec;
-  const int head = blockIdx.x % p.q_heads;
-  const int j = blockIdx.x / p.q_heads;       // query of its request
-  const int r = blockIdx.y;
-  const int start = p.q_start ? min(max(p.q_start[r], 0), p.n_tokens) : r;
-  const int end = p.q_start ? min(max(p.q_start[r + 1], 0), p.n_tokens) : r + 1;
-  const int n_q = end - start;
-  if (j >= n_q) return;
-  const int len = min(max(p.kv_len[r], 0), p.max_len);
-  const int64_t sees = p.causal ? min(static_cast<int64_t>(len) - n_q + j + 1,
-                                      static_cast<int64_t>(len)) : len;
-  const int64_t row = start + j;
-
-  float qa[8], qb[8], ta[8], tb[8];
-  const char* src = p.q + row * p.q_token + head * p.q_head + 8 * sub * ES;
-  load8<DT>(src, qa);
-  load8<DT>(src + 64 * ES, qb);
-  int turned_by = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    ta[i] = qa[i];
-    tb[i] = qb[i];
-  }
-  const int kh = head / p.group;
-  float m = -INFINITY, l = 0.0f, oa[8] = {}, ob[8] = {};
-  for (int64_t t0 = 0; t0 < sees; t0 += kVecsPerWave) {
-    const int64_t t = t0 + grp;
-    const bool in = t < sees;
-    const int b = static_cast<int>((in ? t : sees - 1) / p.block_tokens);
-    const int at = static_cast<int>((in ? t : sees - 1) - static_cast<int64_t>(b) * p.block_tokens);
-    const int entry = p.table[r * p.table_stride + b];
-    const bool live = in && entry >= 0 && entry < p.n_blocks;
-    if (!live) continue;       // this group of lanes sits the step out
-    if (p.delta) {
-      const int d = p.delta[r * p.table_stride + b];
-      if (d != turned_by) {
-        float cs[8], sn[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ta[i] = qa[i];
-          tb[i] = qb[i];
-          cos_sin(d, p.theta[lane_pair(PAIRS, sub, i)], &cs[i], &sn[i]);
-          sn[i] = -sn[i];
-        }
-        turn_runs<PAIRS>(ta, tb, cs, sn);
-        turned_by = d;
-      }
-    }
-    const uint8_t* rec = p.rec + entry * p.rec_block;
-    const int v = at * p.n_heads + kh;
-    const uint16_t* scales = reinterpret_cast<const uint16_t*>(rec + 2LL * p.vecs * CB);
-    const float ks = f16_bits_to_f32(scales[v]);
-    const float vs = f16_bits_to_f32(scales[static_cast<int64_t>(p.vecs) + v]);
-    float a[8], c[8];
-    load_vector<FMT>(rec, v, sub, a, c);
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dot = __builtin_fmaf(a[i], ta[i], dot);
-      dot = __builtin_fmaf(c[i], tb[i], dot);
-    }
-    dot += __shfl_xor(dot, 1, kLanesPerVec);
-    dot += __shfl_xor(dot, 2, kLanesPerVec);
-    dot += __shfl_xor(dot, 4, kLanesPerVec);
-    const float s = dot * (ks * p.scale_log2);
-    const float m_new = fmaxf(m, s);
-    const float keep = m == m_new ? 1.0f : exp2f(m - m_new);
-    const float w = exp2f(s - m_new);
-    load_vector<FMT>(rec + static_cast<int64_t>(p.vecs) * CB, v, sub, a, c);
-    l = l * keep + w;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      oa[i] = oa[i] * keep + w * vs * a[i];
-      ob[i] = ob[i] * keep + w * vs * c[i];
-    }
-    m = m_new;
-  }
-#pragma unroll
-  for (int off = kLanesPerVec; off < kWave; off <<= 1) {
-    const float mo = __shfl_xor(m, off);
-    const float m_new = fmaxf(m, mo);
-    const float own = m == m_new ? 1.0f : exp2f(m - m_new);
-    const float other = mo == m_new ? 1.0f : exp2f(mo - m_new);
-    l = l * own + __shfl_xor(l, off) * other;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      oa[i] = oa[i] * own + __shfl_xor(oa[i], off) * other;
-      ob[i] = ob[i] * own + __shfl_xor(ob[i], off) * other;
-    }
-    m = m_new;
-  }
-  const bool empty = l == 0.0f;
-  const float inv = empty ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    oa[i] *= inv;
-    ob[i] *= inv;
-  }
-  if (grp == 0) {
-    char* dst = p.out + row * p.o_token + head * p.o_head + 8 * sub * ES;
-    store8<DT>(dst, oa);
-    store8<DT>(dst + 64 * ES, ob);
-    if (p.lse && sub == 0)
-      p.lse[row * p.q_heads + head] =
-          empty ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-  }
+int64_t prefix_bytes(const hkv_requests& req) {
+  return (static_cast<int64_t>(req.n_requests + 2) * 8 + 15) / 16 * 16;
 }
 
-template <int FMT, int DT>
-hipError_t launch_pairs(int pairs, const AttendParams& p, dim3 grid, hipStream_t stream) {
-  if (pairs == kInterleaved)
-    hipLaunchKernelGGL((attend_kernel<FMT, DT, kInterleaved>), grid, dim3(kWave), 0, stream, p);
-  else
-    hipLaunchKernelGGL((attend_kernel<FMT, DT, kHalfSplit>), grid, dim3(kWave), 0, stream, p);
-  return hipGetLastError();
-}
-
-template <int FMT>
-hipError_t launch_dtype(int dtype, int pairs, const AttendParams& p, dim3 grid, hipStream_t s) {
-  switch (dtype) {
-    case kF32: return launch_pairs<FMT, kF32>(pairs, p, grid, s);
-    case kF16: return launch_pairs<FMT, kF16>(pairs, p, grid, s);
-    default: return launch_pairs<FMT, kBF16>(pairs, p, grid, s);
-  }
+int64_t share_bytes(const Share& s, const hkv_requests& req) {
+  return s.ranges > 0 ? prefix_bytes(req) + (s.rows * 8 + 15) / 16 * 16 + s.rows * kHeadDim * 4 : 0;
 }
 
 }  // namespace
 
-int64_t attend_workspace_bytes(const Geometry&, const hkv_requests&, int32_t, int32_t, int) {
-  return 0;
+int64_t attend_workspace_bytes(const Geometry& g, const hkv_requests& req, int32_t n_tokens,
+                               int32_t n_q_heads, int dtype) {
+  int64_t most = 0;
+  for (int fmt : {kFP8, kINT4}) {
+    const int64_t b = share_bytes(share_of(fmt, g, req, n_tokens, n_q_heads, dtype), req);
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
@@ -194,13 +153,22 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
   p.block_tokens = c.g.block_tokens;
   p.n_heads = c.g.n_heads;
   p.vecs = c.g.vecs;
+  // ceil(2^(31 + s) / d) with 2^s >= d makes the quotient exact below 2^31
+  int s = 0;
+  while ((int64_t{1} << s) < c.g.block_tokens) ++s;
+  p.block_shift = 31 + s;
+  p.block_magic = ((uint64_t{1} << p.block_shift) + c.g.block_tokens - 1) / c.g.block_tokens;
+  p.n_requests = c.req.n_requests;
   p.table = c.req.block_table;
   p.table_stride = c.req.table_stride;
   p.kv_len = c.req.kv_len;
   p.q_start = c.req.q_start;
-  p.max_len = c.req.max_blocks * c.g.block_tokens;
+  // a pool of no records has no cached tokens
+  p.max_len = c.g.n_blocks > 0 ? c.req.max_blocks * c.g.block_tokens : 0;
   p.max_queries = c.req.max_queries;
   p.n_tokens = c.n_tokens;
+  p.dtype = c.dtype;
+  p.elem = element_size(c.dtype);
   p.q = c.q.data;
   p.out = c.out.data;
   p.q_token = c.q.token;
@@ -213,13 +181,46 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
   p.scale_log2 = static_cast<float>(c.sm_scale * 1.44269504088896340736);
   p.causal = c.causal ? 1 : 0;
   p.delta = c.delta;
+  p.pairs = c.pairs;
   for (int i = 0; i < kHeadDim / 2; ++i)
     p.theta[i] = c.delta ? quarter_turns(c.rope_base, i) : 0.0;
-  const int32_t queries = c.req.max_queries < c.n_tokens ? c.req.max_queries : c.n_tokens;
-  const dim3 grid(static_cast<unsigned>(queries) * c.q.n_heads,
-                  static_cast<unsigned>(c.req.n_requests));
-  return c.fmt == kFP8 ? launch_dtype<kFP8>(c.dtype, c.pairs, p, grid, stream)
-                       : launch_dtype<kINT4>(c.dtype, c.pairs, p, grid, stream);
+
+  const Share share = share_of(c.fmt, c.g, c.req, c.n_tokens, c.q.n_heads, c.dtype);
+  p.set_heads = share.set_heads;
+  p.head_sets = share.head_sets;
+  p.ranges = share.ranges;
+  p.min_tiles = share.min_tiles;
+  p.part_rows = share.part_rows;
+  p.prefix_out = nullptr;
+  p.part_ml = nullptr;
+  p.part_o = nullptr;
+  size_t bytes = kRowsWaves * kWaveAreaBytes + (kRowsWaves / 2) * share.nt * (8192 + 512);
+  dim3 grid;
+  if (share.ranges > 0) {
+    char* ws = static_cast<char*>(c.workspace);
+    p.prefix_out = reinterpret_cast<uint64_t*>(ws);
+    ws += prefix_bytes(c.req);
+    p.part_ml = reinterpret_cast<float*>(ws);
+    p.part_o = reinterpret_cast<float*>(ws + (share.rows * 8 + 15) / 16 * 16);
+    bytes += static_cast<size_t>(prefix_bytes(c.req));
+    grid = dim3(static_cast<unsigned>(share.ranges * share.head_sets));
+  } else {
+    // items beyond 65,535 sets of workgroups are taken in turn
+    int64_t x = share.items;
+    const int64_t most = 65535 / share.head_sets;
+    x = x < most ? x : most;
+    x = x < 1 ? 1 : x;
+    grid = dim3(static_cast<unsigned>(x * share.head_sets), static_cast<unsigned>(c.req.n_requests));
+  }
+  const hipError_t e = c.fmt == kFP8 ? launch_rows_fp8(p, share.nt, grid, bytes, stream)
+                                     : launch_rows_int4(p, share.nt, grid, bytes, stream);
+  if (e != hipSuccess || share.ranges == 0) return e;
+  const int64_t queries = c.req.max_queries < c.n_tokens ? c.req.max_queries : c.n_tokens;
+  hipLaunchKernelGGL(attend_join_kernel,
+                     dim3(static_cast<unsigned>(queries * c.q.n_heads),
+                          static_cast<unsigned>(c.req.n_requests)),
+                     dim3(kJoinWaves * kWave), 0, stream, p, 16 * share.nt);
+  return hipGetLastError();
 }
 
 }  // namespace hkv
