@@ -5,11 +5,13 @@
 namespace hkv {
 namespace {
 
-// One workgroup per row that more than one range worked on: each wave takes
-// every fourth partial result, a lane two dims; then the waves join in order.
-constexpr int kJoinWaves = 4;
+// One workgroup per row that more than one range worked on: its waves (up to
+// 8, by how many partial results a row may have) take the partial results in
+// turn, a lane two dims; then the waves join in order.
+constexpr int kJoinMost = 8;
 
-__global__ __launch_bounds__(kJoinWaves * kWave) void attend_join_kernel(AttendParams p, int item_rows) {
+__global__ __launch_bounds__(kJoinMost * kWave) void attend_join_kernel(AttendParams p, int item_rows,
+                                                                        int waves) {
   const int r = blockIdx.y;
   const Span s = span_of(p, r);
   const int j = blockIdx.x / p.q_heads;
@@ -18,33 +20,33 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void attend_join_kernel(AttendP
   const int kh = head / p.group;
   const int row = j * p.group + (head - kh * p.group);
   const int item = row / item_rows;
-  const uint64_t tiles = tiles_of(s);
-  const uint64_t f0 = p.prefix_out[r] + item * tiles;
-  const uint64_t per = p.prefix_out[p.n_requests + 1];
-  const int64_t w0 = f0 / per, w1 = (f0 + tiles - 1) / per;
+  const uint32_t tiles = tiles_of(s);
+  const uint32_t f0 = p.prefix_out[r] + item * tiles;
+  const uint32_t per = p.prefix_out[p.n_requests + 1];
+  const int w0 = f0 / per, w1 = (f0 + tiles - 1) / per;
   if (w0 == w1) return;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = threadIdx.x / kWave;
   const int64_t in_item = row - item * item_rows;
-  auto at = [&](int64_t w) {
-    const int64_t which = w == w0 && f0 > static_cast<uint64_t>(w0) * per ? 1 : 0;
-    return ((w * 2 + which) * p.n_heads + kh) * p.part_rows + in_item;
+  auto at = [&](int w) {
+    const int which = w == w0 && f0 > w0 * per ? 1 : 0;
+    return (static_cast<int64_t>(w * 2 + which) * p.n_heads + kh) * p.part_rows + in_item;
   };
   float m = kNoReference, l = 0.0f;
   float2 o = make_float2(0.0f, 0.0f);
   constexpr int kBatch = 8;
-  for (int64_t w = w0 + wave; w <= w1; w += kJoinWaves * kBatch) {
+  for (int w = w0 + wave; w <= w1; w += waves * kBatch) {
     float2 ml[kBatch], x[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = at(min(w + u * kJoinWaves, w1));
+      const int64_t i = at(min(w + u * waves, w1));
       ml[u] = reinterpret_cast<const float2*>(p.part_ml)[i];
       x[u] = reinterpret_cast<const float2*>(p.part_o + i * kHeadDim)[lane];
     }
     float top = m;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if (w + u * kJoinWaves <= w1) top = fmaxf(top, ml[u].x);
+      if (w + u * waves <= w1) top = fmaxf(top, ml[u].x);
     const float keep = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
     l *= keep;
     o.x *= keep;
@@ -52,24 +54,22 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void attend_join_kernel(AttendP
     m = top;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (w + u * kJoinWaves > w1) break;
+      if (w + u * waves > w1) break;
       const float f = ml[u].x == m ? 1.0f : __builtin_amdgcn_exp2f(ml[u].x - m);
       l += ml[u].y * f;
       o.x += x[u].x * f;
       o.y += x[u].y * f;
     }
   }
-  __shared__ float2 join_ml[kJoinWaves];
-  __shared__ float2 join_o[kJoinWaves][kWave];
+  __shared__ float2 join_ml[kJoinMost];
+  __shared__ float2 join_o[kJoinMost][kWave];
   join_o[wave][lane] = o;
   if (lane == 0) join_ml[wave] = make_float2(m, l);
   __syncthreads();
   if (threadIdx.x >= kHeadDim / 8) return;     // 8 dims a lane
   float top = kNoReference, sum = 0.0f, y[8] = {};
-#pragma unroll
-  for (int w = 0; w < kJoinWaves; ++w) top = fmaxf(top, join_ml[w].x);
-#pragma unroll
-  for (int w = 0; w < kJoinWaves; ++w) {
+  for (int w = 0; w < waves; ++w) top = fmaxf(top, join_ml[w].x);
+  for (int w = 0; w < waves; ++w) {
     const float f = join_ml[w].x == top ? 1.0f : __builtin_amdgcn_exp2f(join_ml[w].x - top);
     sum += join_ml[w].y * f;
 #pragma unroll
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void attend_join_kernel(AttendP
 }
 
 struct Share {
-  int nt;                  // 16 nt rows per item
+  int hp, nt;              // heads per score tile, tiles of 16 rows: 16 nt / hp rows per item
   int set_heads, head_sets, ranges, min_tiles, part_rows;
   int64_t rows;            // partial rows in all
   int64_t items;           // of one request, at most
@@ -102,20 +102,24 @@ Share share_of(int fmt, const Geometry& g, const hkv_requests& req, int32_t n_to
   Share s;
   const int64_t queries = req.max_queries < n_tokens ? req.max_queries : n_tokens;
   const int64_t rows = queries * (n_q_heads / g.n_heads);
+  // Two heads of at most 8 rows share a score tile, which halves the softmax
+  // and the bookkeeping of each.
+    s.hp = rows <= 8 && g.n_heads % 2 == 0 ? 2 : 1;
   s.nt = dtype == kF32 || rows <= 16 ? 1 : 2;
-  const int64_t item_rows = 16 * s.nt;
+  const int64_t item_rows = 16 * s.nt / s.hp;
   s.items = (rows + item_rows - 1) / item_rows;
   const int64_t max_len = static_cast<int64_t>(req.max_blocks) * g.block_tokens;
   const int64_t tiles = max_len < kTileTokens ? 1 : (max_len + kTileTokens - 1) / kTileTokens;
   // Two INT4 heads of a token share a 128-byte line, so one workgroup reads both.
-  s.set_heads = fmt == kINT4 && g.n_heads % 2 == 0 ? 2 : 1;
-  s.head_sets = g.n_heads / s.set_heads;
+  s.set_heads = s.hp == 1 && fmt == kINT4 && g.n_heads % 2 == 0 ? 2 : 1;
+  s.head_sets = g.n_heads / (s.set_heads * s.hp);
   const int64_t phases = kRowsWaves / s.set_heads;
   s.ranges = 0;
-  s.min_tiles = static_cast<int>(2 * phases);
+  s.min_tiles = static_cast<int>(phases);
   s.part_rows = static_cast<int>(rows < item_rows ? rows : item_rows);
-  if (req.n_requests <= kMaxFlatRequests && tiles > 4 * phases && queries * n_q_heads <= (1 << 20)) {
-    const int64_t all = static_cast<int64_t>(req.n_requests) * s.items * tiles;
+  const int64_t all = static_cast<int64_t>(req.n_requests) * s.items * tiles;
+  if (req.n_requests <= kMaxFlatRequests && tiles > 4 * phases && queries * n_q_heads <= (1 << 20) &&
+      all < (int64_t{1} << 30)) {
     int64_t ranges = 512 / s.head_sets;
     const int64_t most = (all + s.min_tiles - 1) / s.min_tiles;
     ranges = ranges < 1 ? 1 : ranges;
@@ -126,7 +130,7 @@ Share share_of(int fmt, const Geometry& g, const hkv_requests& req, int32_t n_to
 }
 
 int64_t prefix_bytes(const hkv_requests& req) {
-  return (static_cast<int64_t>(req.n_requests + 2) * 8 + 15) / 16 * 16;
+  return (static_cast<int64_t>(req.n_requests + 2) * 4 + 15) / 16 * 16;
 }
 
 int64_t share_bytes(const Share& s, const hkv_requests& req) {
@@ -194,11 +198,12 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
   p.prefix_out = nullptr;
   p.part_ml = nullptr;
   p.part_o = nullptr;
+  // the join of the waves needs more than 32 rows' second query parts
   size_t bytes = kRowsWaves * kWaveAreaBytes + (kRowsWaves / 2) * share.nt * (8192 + 512);
   dim3 grid;
   if (share.ranges > 0) {
     char* ws = static_cast<char*>(c.workspace);
-    p.prefix_out = reinterpret_cast<uint64_t*>(ws);
+    p.prefix_out = reinterpret_cast<uint32_t*>(ws);
     ws += prefix_bytes(c.req);
     p.part_ml = reinterpret_cast<float*>(ws);
     p.part_o = reinterpret_cast<float*>(ws + (share.rows * 8 + 15) / 16 * 16);
@@ -212,14 +217,18 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     x = x < 1 ? 1 : x;
     grid = dim3(static_cast<unsigned>(x * share.head_sets), static_cast<unsigned>(c.req.n_requests));
   }
-  const hipError_t e = c.fmt == kFP8 ? launch_rows_fp8(p, share.nt, grid, bytes, stream)
-                                     : launch_rows_int4(p, share.nt, grid, bytes, stream);
+  const hipError_t e = c.fmt == kFP8 ? launch_rows_fp8(p, share.hp, share.nt, grid, bytes, stream)
+                                     : launch_rows_int4(p, share.hp, share.nt, grid, bytes, stream);
   if (e != hipSuccess || share.ranges == 0) return e;
   const int64_t queries = c.req.max_queries < c.n_tokens ? c.req.max_queries : c.n_tokens;
+  // about 8 partial results of a row for each wave
+  const int64_t parts = share.ranges / (static_cast<int64_t>(c.req.n_requests) * share.items);
+  int waves = 1;
+  while (waves < kJoinMost && waves * 8 < parts) waves *= 2;
   hipLaunchKernelGGL(attend_join_kernel,
                      dim3(static_cast<unsigned>(queries * c.q.n_heads),
                           static_cast<unsigned>(c.req.n_requests)),
-                     dim3(kJoinWaves * kWave), 0, stream, p, 16 * share.nt);
+                     dim3(waves * kWave), 0, stream, p, 16 * share.nt / share.hp, waves);
   return hipGetLastError();
 }
 

@@ -6,10 +6,10 @@
 namespace hkv {
 
 constexpr int kTileTokens = 32;        // tokens of a step of the rows kernel
-constexpr int kRowsWaves = 8;
+constexpr int kRowsWaves = 4;
 constexpr int kRowsThreads = kRowsWaves * 64;
 constexpr int kMaxFlatRequests = 1024; // requests whose tiles are dealt out evenly
-constexpr int kWaveAreaBytes = 1024;   // LDS of a wave of the rows kernel
+constexpr int kWaveAreaBytes = 1280;   // LDS of a wave of the rows kernel
 
 struct AttendParams {
   const uint8_t* rec;
@@ -36,19 +36,19 @@ struct AttendParams {
   const int32_t* delta;    // NULL: stored positions stand
   int32_t pairs;
   // the rows kernel's share of the work
-  int32_t set_heads, head_sets;   // key heads per workgroup, sets of them
+  int32_t set_heads, head_sets;   // waves of different heads in a workgroup, sets of heads
   int32_t ranges;          // > 0: all tiles dealt out over this many ranges
   int32_t min_tiles;       // least tiles of a range
   int32_t part_rows;       // rows per head of a partial result
-  uint64_t* prefix_out;    // [n_requests + 2]: first tile of each request, total, tiles per range
+  uint32_t* prefix_out;    // [n_requests + 2]: first tile of each request, total, tiles per range
   float* part_ml;          // reference and sum of each partial row
   float* part_o;           // its weighted values
   double theta[64];
 };
 
-hipError_t launch_rows_int4(const AttendParams& p, int nt, dim3 grid, size_t bytes,
+hipError_t launch_rows_int4(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                             hipStream_t stream);
-hipError_t launch_rows_fp8(const AttendParams& p, int nt, dim3 grid, size_t bytes,
+hipError_t launch_rows_fp8(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                            hipStream_t stream);
 
 }  // namespace hkv

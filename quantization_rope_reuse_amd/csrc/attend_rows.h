@@ -74,51 +74,37 @@ __device__ __forceinline__ h8 fp8_run(uint32_t lo, uint32_t hi) {
 }
 
 // 8 dims x 8 tokens of V, one (INT4) or two (FP8) dwords per token, as 8
-// operands: out[t] holds dim t of tokens 0 .. 7.
-template <int FMT, int W>
-__device__ __forceinline__ void transpose_run(const uint32_t (&v)[8][W], h8 (&out)[8]) {
-  h2 part[8][4];
+// operands of which this makes four: out[t] holds dim 4 HALF + t of tokens
+// 0 .. 7.
+template <int FMT, int HALF, int W>
+__device__ __forceinline__ void transpose_run(const uint32_t (&v)[8][W], h8 (&out)[4]) {
+  h2 part[4][4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if constexpr (FMT == kINT4) {
-      const uint32_t lo = __builtin_amdgcn_perm(v[2 * k + 1][0], v[2 * k][0], 0x05040100u);
-      const uint32_t hi = __builtin_amdgcn_perm(v[2 * k + 1][0], v[2 * k][0], 0x07060302u);
-      const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-      part[0][k] = nibble_low(lo);
-      part[1][k] = nibble_high(lo);
-      part[2][k] = nibble_low(lo8);
-      part[3][k] = nibble_high(lo8);
-      part[4][k] = nibble_low(hi);
-      part[5][k] = nibble_high(hi);
-      part[6][k] = nibble_low(hi8);
-      part[7][k] = nibble_high(hi8);
+      const uint32_t x = __builtin_amdgcn_perm(v[2 * k + 1][0], v[2 * k][0],
+                                               HALF == 0 ? 0x05040100u : 0x07060302u);
+      const uint32_t y = x >> 8;
+      part[0][k] = nibble_low(x);
+      part[1][k] = nibble_high(x);
+      part[2][k] = nibble_low(y);
+      part[3][k] = nibble_high(y);
     } else {
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const uint32_t x = __builtin_amdgcn_perm(v[2 * k + 1][d], v[2 * k][d], 0x05010400u);
-        const uint32_t y = __builtin_amdgcn_perm(v[2 * k + 1][d], v[2 * k][d], 0x07030602u);
-        part[4 * d + 0][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, false);
-        part[4 * d + 1][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, true);
-        part[4 * d + 2][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.0f, false);
-        part[4 * d + 3][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.0f, true);
-      }
+      constexpr int d = W == 2 ? HALF : 0;
+      const uint32_t x = __builtin_amdgcn_perm(v[2 * k + 1][d], v[2 * k][d], 0x05010400u);
+      const uint32_t y = __builtin_amdgcn_perm(v[2 * k + 1][d], v[2 * k][d], 0x07030602u);
+      part[0][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, false);
+      part[1][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, true);
+      part[2][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.0f, false);
+      part[3][k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.0f, true);
     }
   }
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
+  for (int t = 0; t < 4; ++t)
     out[t] = h8{part[t][0][0], part[t][0][1], part[t][1][0], part[t][1][1],
                 part[t][2][0], part[t][2][1], part[t][3][0], part[t][3][1]};
 }
 
-__device__ __forceinline__ void load8_16bit(bool f16, const char* p, float (&x)[8]) {
-  const u32x4 a = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t w = a[j];
-    x[2 * j] = f16 ? f16_bits_to_f32(w & 0xFFFFu) : bf16_bits_to_f32(w & 0xFFFFu);
-    x[2 * j + 1] = f16 ? f16_bits_to_f32(w >> 16) : bf16_bits_to_f32(w >> 16);
-  }
-}
 __device__ __forceinline__ void store8_any(int dtype, char* p, const float (&x)[8]) {
   if (dtype == kF32)
     store8<kF32>(p, x);
@@ -126,6 +112,12 @@ __device__ __forceinline__ void store8_any(int dtype, char* p, const float (&x)[
     store8<kF16>(p, x);
   else
     store8<kBF16>(p, x);
+}
+
+// A buffer from a wave-uniform address on: loads take a 32-bit offset per lane
+// and one per wave, with no address arithmetic of their own.
+__device__ __forceinline__ auto buffer_at(const uint8_t* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, 0xFFFFFFFFu, 0x00027000);
 }
 
 struct Span {            // a request's queries and cached tokens
@@ -187,73 +179,75 @@ __device__ __forceinline__ void merge_rows(RowState<NT>& a, const f32x4* o, cons
   }
 }
 
-// QP, PP: fp16 parts of a query and of a weight.  TM: how block_tokens and
+// QP, PP: fp16 parts of a query and of a weight (two for fp32).  TM: how block_tokens and
 // the tile of 32 tokens fit: kWhole, a tile lies in one block; kEighths,
 // runs of 8 tokens do; kAny.
 enum TileMode { kWhole = 0, kEighths = 1, kAny = 2 };
 
-template <int FMT, int NT, int QP, int PP, int TM>
+template <int FMT, int DT, int HP, int NT, int QP, int TM>
 __global__ __launch_bounds__(kRowsThreads, 2)
 void attend_rows_kernel(AttendParams p) {
   constexpr int CB = FMT == kFP8 ? kHeadDim : kHeadDim / 2;
   constexpr int W = CB / 64;                  // dwords per 8 codes
-  constexpr int kItemRows = 16 * NT;
-  extern __shared__ char lds[];
-  // per wave: scales of a tile (64 floats), token offsets (32 int64),
-  // cosines and sines (64 float2); then the merge area; then the prefix
-  struct WaveArea {
-    float scale[2][kTileTokens];
+  constexpr int ES = ElemSize<DT>::value;
+  constexpr int PP = DT == kF32 ? 2 : 1;
+  static_assert(HP == 1 || NT == 1, "two heads share one score tile");
+  constexpr int kItemRows = 16 * NT / HP;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  // per wave: a WaveArea; then the merge area; then the prefix
+  struct alignas(16) WaveArea {
+    float scale[2][2][kTileTokens];      // K, V; head; token
     int64_t offset[kTileTokens];
     float2 turn[kHeadDim / 2];
   };
   static_assert(sizeof(WaveArea) == kWaveAreaBytes, "host LDS size");
   const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform
   const int c = lane & 15, g = lane >> 4;
   WaveArea& area = reinterpret_cast<WaveArea*>(lds)[wave];
   char* merge = lds + kRowsWaves * sizeof(WaveArea);
   f32x4* merge_o = reinterpret_cast<f32x4*>(merge);
   float2* merge_ml = reinterpret_cast<float2*>(merge + (kRowsWaves / 2) * NT * 8192);
-  uint64_t* prefix = reinterpret_cast<uint64_t*>(merge + (kRowsWaves / 2) * NT * (8192 + 512));
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(merge + (kRowsWaves / 2) * NT * (8192 + 512));
 
   const int set = blockIdx.x % p.head_sets;
   const int range = blockIdx.x / p.head_sets;
   const int sub = wave % p.set_heads;
   const int phase = wave / p.set_heads;
   const int phases = kRowsWaves / p.set_heads;
-  const int kh = set * p.set_heads + sub;
+  const int kh0 = (set * p.set_heads + sub) * HP;      // the wave's first key head
   const int64_t token_bytes = static_cast<int64_t>(p.n_heads) * CB;
 
   // The work: this workgroup's range of the tiles of all items, or (one
   // request per blockIdx.y) whole items.
-  uint64_t at, end, per = 0, stride = 0;
-  int r;
+  uint32_t at = 0, end = 0;            // flat tiles
+  int r, item = range, items = 0;
   if (p.ranges > 0) {
     const int R = p.n_requests;
     constexpr int kPer = kMaxFlatRequests / kRowsThreads;
-    uint64_t own[kPer], sum = 0;
+    uint32_t own[kPer], sum = 0;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int q = threadIdx.x * kPer + u;
       own[u] = 0;
       if (q < R) {
         const Span s = span_of(p, q);
-        own[u] = static_cast<uint64_t>((s.rows + kItemRows - 1) / kItemRows) * tiles_of(s);
+        own[u] = static_cast<uint32_t>((s.rows + kItemRows - 1) / kItemRows) * tiles_of(s);
       }
       sum += own[u];
     }
-    uint64_t run = sum;
+    uint32_t run = sum;
     if (R > 1) {
 #pragma unroll
       for (int off = 1; off < kWave; off <<= 1) {
-        const uint64_t o = __shfl_up(run, off);
+        const uint32_t o = __shfl_up(run, off);
         if (lane >= off) run += o;
       }
     }
-    uint64_t* wave_sum = reinterpret_cast<uint64_t*>(merge);
+    uint32_t* wave_sum = reinterpret_cast<uint32_t*>(merge);
     if (lane == kWave - 1) wave_sum[wave] = run;
     __syncthreads();
-    uint64_t before = run - sum;
+    uint32_t before = run - sum;
     for (int w = 0; w < wave; ++w) before += wave_sum[w];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
@@ -263,11 +257,10 @@ void attend_rows_kernel(AttendParams p) {
     }
     if (R == kMaxFlatRequests && threadIdx.x == kRowsThreads - 1) prefix[R] = before;
     __syncthreads();
-    const uint64_t total = prefix[R];
-    per = (total + p.ranges - 1) / p.ranges;
-    if (per < static_cast<uint64_t>(p.min_tiles)) per = p.min_tiles;
-    at = range * per;
-    end = at + per < total ? at + per : total;
+    const uint32_t total = prefix[R];
+    const uint32_t per = max((total + p.ranges - 1) / p.ranges, static_cast<uint32_t>(p.min_tiles));
+    at = min(range * per, total);       // range * per < total + per * ranges: below 2^32
+    end = min(at + per, total);
     if (p.prefix_out && blockIdx.x == 0) {
       for (int q = threadIdx.x; q <= R; q += kRowsThreads) p.prefix_out[q] = prefix[q];
       if (threadIdx.x == 0) p.prefix_out[R + 1] = per;
@@ -284,28 +277,25 @@ void attend_rows_kernel(AttendParams p) {
     r = lo;
   } else {
     r = blockIdx.y;
-    const Span s = span_of(p, r);
-    const uint64_t tiles = tiles_of(s);
-    at = range * tiles;
-    end = static_cast<uint64_t>((s.rows + kItemRows - 1) / kItemRows) * tiles;
-    stride = static_cast<uint64_t>(gridDim.x / p.head_sets) * tiles;
-    if (at >= end) return;
+    items = (span_of(p, r).rows + kItemRows - 1) / kItemRows;
   }
 
-  const uint64_t first_at = at;
+  const uint32_t first_at = at;
   bool again = false;
-  while (at < end) {
+  while (p.ranges > 0 ? at < end : item < items) {
     if (again) __syncthreads();          // the merge area is free again
     again = true;
     if (p.ranges > 0)
       while (prefix[r + 1] <= at) ++r;   // requests without items
     const Span s = span_of(p, r);
     const int tiles = tiles_of(s);
-    const uint64_t in_request = p.ranges > 0 ? at - prefix[r] : at;
-    const int item = static_cast<int>(in_request / tiles);
-    const int t0 = static_cast<int>(in_request - static_cast<uint64_t>(item) * tiles);
+    int t0 = 0;
+    if (p.ranges > 0) {
+      item = (at - prefix[r]) / static_cast<uint32_t>(tiles);
+      t0 = at - prefix[r] - item * tiles;
+    }
     int t1 = tiles;
-    if (p.ranges > 0 && end - at < static_cast<uint64_t>(tiles - t0))
+    if (p.ranges > 0 && end - at < static_cast<uint32_t>(tiles - t0))
       t1 = t0 + static_cast<int>(end - at);
     const bool whole = t0 == 0 && t1 == tiles;
     const int row0 = item * kItemRows;
@@ -317,12 +307,12 @@ void attend_rows_kernel(AttendParams p) {
     int last = 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int row = row0 + 16 * n + c;
+      const int row = row0 + 16 * n + (HP == 2 ? c & 7 : c);
       real[n] = row < s.rows;
       const int clamped = min(row, s.rows - 1);
       const int j = clamped / p.group;
       query[n] = s.start + j;
-      head[n] = kh * p.group + (clamped - j * p.group);
+      head[n] = (HP == 2 ? kh0 + (c >> 3) : kh0) * p.group + (clamped - j * p.group);
       q_row[n] = p.q + query[n] * p.q_token + head[n] * p.q_head;
       sees[n] = max(p.causal ? s.len - s.n_q + j + 1 : s.len, 0);
     }
@@ -332,84 +322,85 @@ void attend_rows_kernel(AttendParams p) {
     const int sees_most = p.causal ? s.len - s.n_q + j_last + 1 : s.len;
     last = min(t1, max(sees_most, 0) / kTileTokens + (max(sees_most, 0) % kTileTokens != 0));
 
-    const int32_t* table = p.table + r * p.table_stride;
-    const int32_t* moves = p.delta ? p.delta + r * p.table_stride : nullptr;
     // Queries as operands: dims 32 g + 8 kk + (0 .. 7) in the order of the
     // codes, times 2^-e.  The row's exponent puts its largest magnitude below
     // 2^14, so a turned one stays below 2^15; fp16 queries that do not turn
     // are operands as they are.
-    h8 qf[NT][QP][4];
+    // (second parts of 32 rows: in LDS, they do not fit the registers)
+    constexpr bool kLowInLds = NT * QP == 4;
+    h8 qf[NT][kLowInLds ? 1 : QP][4];
+    h8* low = reinterpret_cast<h8*>(merge) + wave * NT * 4 * kWave + lane;
     int e[NT];
     float grow[NT];                       // 2^e
-    auto load_run = [&](const char* src, float (&x)[8]) __attribute__((always_inline)) {
-      if constexpr (PP > 1)
-        load8<kF32>(src, x);
-      else
-        load8_16bit(p.dtype == kF16, src, x);
+    const int32_t* table = p.table + r * p.table_stride;
+    const int32_t* moves = p.delta ? p.delta + r * p.table_stride : nullptr;
+    auto to_operand = [&](const float (&x)[8], int n, int kk) __attribute__((always_inline)) {
+      h8 second;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+        const float v = __builtin_ldexpf(x[FMT == kINT4 ? kOrder[j] : j], -e[n]);
+        const _Float16 hi = static_cast<_Float16>(v);
+        qf[n][0][kk][j] = hi;
+        if constexpr (QP > 1) second[j] = static_cast<_Float16>(v - static_cast<float>(hi));
+      }
+      if constexpr (kLowInLds)
+        low[(n * 4 + kk) * kWave] = second;
+      else if constexpr (QP > 1)
+        qf[n][1][kk] = second;
     };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float top = 0.0f;
+      float x[4][8], top = 0.0f;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        float x[8];
-        load_run(q_row[n] + (32 * g + 8 * kk) * p.elem, x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-      }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
+      for (int kk = 0; kk < 4; ++kk) load8<DT>(q_row[n] + (32 * g + 8 * kk) * ES, x[kk]);
       e[n] = 0;
-      if (!(QP == 1 && p.dtype == kF16) && top > 0.0f && top < INFINITY)
-        e[n] = max(__builtin_amdgcn_frexp_expf(top) - 14, -100);
-      grow[n] = __builtin_ldexpf(1.0f, e[n]);
-    }
-    auto load_queries = [&](int delta) __attribute__((always_inline)) {
-      if (QP > 1 && moves) {
-        float cc, ss;
-        cos_sin(delta, p.theta[lane], &cc, &ss);
-        wave_lds_fence();
-        area.turn[lane] = make_float2(cc, -ss);
-        wave_lds_fence();
+      if constexpr (!(QP == 1 && DT == kF16)) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[kk][j]));
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (top > 0.0f && top < INFINITY) e[n] = max(__builtin_amdgcn_frexp_expf(top) - 14, -100);
       }
+      grow[n] = __builtin_ldexpf(1.0f, e[n]);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) to_operand(x[kk], n, kk);
+    }
+    // the queries turned by -delta
+    auto turn_queries = [&](int delta) __attribute__((always_inline)) {
+      float cc, ss;
+      cos_sin(delta, p.theta[lane], &cc, &ss);
+      wave_lds_fence();
+      area.turn[lane] = make_float2(cc, -ss);
+      wave_lds_fence();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          float x[8];
-          load_run(q_row[n] + (32 * g + 8 * kk) * p.elem, x);
-          if (QP > 1 && moves) {
-            if (p.pairs == kInterleaved) {
+          float x[8], y[8];
+          load8<DT>(q_row[n] + (32 * g + 8 * kk) * ES, x);
+          if (p.pairs == kInterleaved) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 t = area.turn[16 * g + 4 * kk + j];
-                turn_pair(x[2 * j], x[2 * j + 1], t.x, t.y);
-              }
-            } else {
-              float y[8];
-              load_run(q_row[n] + (32 * (g ^ 2) + 8 * kk) * p.elem, y);
+            for (int j = 0; j < 4; ++j) {
+              const float2 t = area.turn[16 * g + 4 * kk + j];
+              turn_pair(x[2 * j], x[2 * j + 1], t.x, t.y);
+            }
+          } else {
+            load8<DT>(q_row[n] + (32 * (g ^ 2) + 8 * kk) * ES, y);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float2 t = area.turn[32 * (g & 1) + 8 * kk + j];
-                float a = g < 2 ? x[j] : y[j], b = g < 2 ? y[j] : x[j];
-                turn_pair(a, b, t.x, t.y);
-                x[j] = g < 2 ? a : b;
-              }
+            for (int j = 0; j < 8; ++j) {
+              const float2 t = area.turn[32 * (g & 1) + 8 * kk + j];
+              float a = g < 2 ? x[j] : y[j], b = g < 2 ? y[j] : x[j];
+              turn_pair(a, b, t.x, t.y);
+              x[j] = g < 2 ? a : b;
             }
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
-            const float v = __builtin_ldexpf(x[FMT == kINT4 ? kOrder[j] : j], -e[n]);
-            const _Float16 hi = static_cast<_Float16>(v);
-            qf[n][0][kk][j] = hi;
-            if constexpr (QP > 1) qf[n][1][kk][j] = static_cast<_Float16>(v - static_cast<float>(hi));
-          }
+          to_operand(x, n, kk);
         }
     };
     int turned_by = 0;
-    bool loaded = false;
-    if (QP == 1) load_queries(0);
 
     RowState<NT> st;
 #pragma unroll
@@ -443,15 +434,15 @@ void attend_rows_kernel(AttendParams p) {
       a.delta = QP > 1 && moves ? moves[a.block] : 0;
       return a;
     };
-    struct Raw {
-      u32x4 k[2][W];
-      uint32_t v[8][W];
+    struct Keys {
+      u32x4 k[HP][2][W];
       uint32_t scale;
       uint32_t live;                    // tokens of the tile that exist
       int delta;
+      const uint8_t* v;                 // this lane's values: first token (not kAny)
     };
-    auto fetch = [&](int t, const Place& a) __attribute__((always_inline)) {
-      Raw x;
+    auto fetch_keys = [&](int t, const Place& a) __attribute__((always_inline)) {
+      Keys x;
       const bool ok = static_cast<uint32_t>(a.entry) < static_cast<uint32_t>(p.n_blocks) &&
                       (lane & 31) < s.len - t * kTileTokens;
       x.live = static_cast<uint32_t>(__ballot(ok));
@@ -461,38 +452,33 @@ void attend_rows_kernel(AttendParams p) {
       if constexpr (TM == kWhole) {
         const uint8_t* rec = p.rec + __builtin_amdgcn_readfirstlane(entry) * p.rec_block;
         const int inside = __builtin_amdgcn_readfirstlane(a.inside);
-        const uint8_t* kb = rec + inside * token_bytes + kh * CB;
+        const uint8_t* kb = rec + inside * token_bytes + kh0 * CB;
+        x.v = kb + v_off;
+        const auto keys = buffer_at(kb);
         const uint32_t krow = (8 * (c >> 2) + (c & 3)) * static_cast<uint32_t>(token_bytes) + g * (CB / 4);
-        const uint32_t vrow = 8 * g * static_cast<uint32_t>(token_bytes) + c * (CB / 16);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int h = 0; h < HP; ++h)
 #pragma unroll
-          for (int w = 0; w < W; ++w)
-            x.k[u][w] = *reinterpret_cast<const u32x4*>(kb + 4 * u * token_bytes + (krow + 16 * w));
-        const uint8_t* vb = kb + v_off;
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(vb + k * token_bytes + vrow);
-          if constexpr (W == 1) {
-            x.v[k][0] = src[0];
-          } else {
-            const u32x2 y = *reinterpret_cast<const u32x2*>(src);
-            x.v[k][0] = y[0];
-            x.v[k][1] = y[1];
-          }
-        }
-        const uint16_t* scales = reinterpret_cast<const uint16_t*>(rec + 2 * v_off) +
-                                 (static_cast<int64_t>(inside) * p.n_heads + kh);
-        x.scale = scales[(lane < 32 ? 0 : p.vecs) + (lane & 31) * p.n_heads];
+            for (int w = 0; w < W; ++w)
+              x.k[h][u][w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                  keys, krow + h * CB + 16 * w, 4 * u * static_cast<uint32_t>(token_bytes), 0));
+        const auto scales = buffer_at(rec + 2 * v_off + 2 * (static_cast<int64_t>(inside) * p.n_heads + kh0));
+        const int at2 = 2 * ((lane < 32 ? 0 : p.vecs) + (lane & 31) * p.n_heads);
+        // (two heads' scales lie side by side: one word)
+        if constexpr (HP == 2)
+          x.scale = __builtin_amdgcn_raw_buffer_load_b32(scales, at2, 0, 0);
+        else
+          x.scale = __builtin_amdgcn_raw_buffer_load_b16(scales, at2, 0, 0);
       } else {
         const uint8_t* rec = p.rec + entry * p.rec_block;
         wave_lds_fence();
         if (lane < kTileTokens) area.offset[lane] = entry * p.rec_block + a.inside * token_bytes;
         wave_lds_fence();
-        const uint8_t* kb = p.rec + kh * CB + g * (CB / 4);
-        const uint8_t* vb = p.rec + kh * CB + c * (CB / 16) + v_off;
+        const uint8_t* kb = p.rec + kh0 * CB + g * (CB / 4);
         const int64_t k0 = area.offset[8 * (c >> 2) + (TM == kAny ? c & 3 : 0)];
-        const int64_t v0 = area.offset[8 * g];
+        x.v = p.rec + kh0 * CB + c * (CB / 16) + v_off + (TM == kEighths ? area.offset[8 * g] : 0);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint8_t* src;
@@ -501,81 +487,141 @@ void attend_rows_kernel(AttendParams p) {
           else
             src = kb + (u == 0 ? k0 : area.offset[8 * (c >> 2) + 4 + (c & 3)]);
 #pragma unroll
-          for (int w = 0; w < W; ++w) x.k[u][w] = *reinterpret_cast<const u32x4*>(src + 16 * w);
-        }
+          for (int h = 0; h < HP; ++h)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint8_t* at8 = vb + (TM == kEighths ? v0 + k * token_bytes : area.offset[8 * g + k]);
-          if constexpr (W == 1) {
-            x.v[k][0] = *reinterpret_cast<const uint32_t*>(at8);
-          } else {
-            const u32x2 y = *reinterpret_cast<const u32x2*>(at8);
-            x.v[k][0] = y[0];
-            x.v[k][1] = y[1];
-          }
+            for (int w = 0; w < W; ++w)
+              x.k[h][u][w] = *reinterpret_cast<const u32x4*>(src + h * CB + 16 * w);
         }
-        x.scale = reinterpret_cast<const uint16_t*>(rec + 2 * v_off)[
-            (lane < 32 ? 0 : p.vecs) + a.inside * p.n_heads + kh];
+        const uint16_t* scales = reinterpret_cast<const uint16_t*>(rec + 2 * v_off) +
+                                 (lane < 32 ? 0 : p.vecs) + a.inside * p.n_heads + kh0;
+        if constexpr (HP == 2)
+          x.scale = *reinterpret_cast<const uint32_t*>(scales);
+        else
+          x.scale = *scales;
       }
       return x;
     };
 
-    auto scores = [&](const h8 (&kf)[2][4], f32x4 (&acc)[NT][2]) __attribute__((always_inline)) {
+    // (kAny: the tokens' offsets, in LDS since fetch_keys)
+    auto fetch_values = [&](const Keys& x, uint32_t (&v)[HP][8][W]) __attribute__((always_inline)) {
+      const uint32_t vrow = 8 * g * static_cast<uint32_t>(token_bytes) + c * (CB / 16);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int h = 0; h < HP; ++h)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int qp = QP - 1; qp >= 0; --qp)
-              a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u][kk], qf[n][qp][kk], a, 0, 0, 0);
-          acc[n][u] = a;
+        for (int k = 0; k < 8; ++k) {
+          if constexpr (TM == kWhole) {
+            const auto values = buffer_at(x.v);
+            const uint32_t at8 = k * static_cast<uint32_t>(token_bytes);
+            if constexpr (W == 1) {
+              v[h][k][0] = __builtin_amdgcn_raw_buffer_load_b32(values, vrow + h * CB, at8, 0);
+            } else {
+              const u32x2 y = __builtin_bit_cast(
+                  u32x2, __builtin_amdgcn_raw_buffer_load_b64(values, vrow + h * CB, at8, 0));
+              v[h][k][0] = y[0];
+              v[h][k][1] = y[1];
+            }
+          } else {
+            const uint8_t* src = x.v + h * CB + (TM == kEighths ? k * token_bytes : area.offset[8 * g + k]);
+            if constexpr (W == 1) {
+              v[h][k][0] = *reinterpret_cast<const uint32_t*>(src);
+            } else {
+              const u32x2 y = *reinterpret_cast<const u32x2*>(src);
+              v[h][k][0] = y[0];
+              v[h][k][1] = y[1];
+            }
+          }
         }
     };
 
-    auto compute = [&](int t, Raw& x) __attribute__((always_inline)) {
-      // wave-uniform
-      const bool part = x.live != 0xFFFFFFFFu || sees_least < kTileTokens ||
-                        t * kTileTokens > sees_least - kTileTokens;
-      // scales through LDS: lane's token -> the 8 tokens of its group;
-      // those of tokens that do not exist become 0
-      const float sc = (x.live >> (lane & 31)) & 1 ? f16_bits_to_f32(x.scale) : 0.0f;
-      wave_lds_fence();
-      area.scale[lane >> 5][lane & 31] = sc * (lane < 32 ? p.scale_log2 : kWeightScale);
-      wave_lds_fence();
-      h8 kf[2][4];
+    // The scores of a tile.  Of two heads' a lane keeps its own head's: columns
+    // 0..7 are rows of the first, 8..15 of the second.  The barriers keep the
+    // operands of a step from being made before the last ones are used, which
+    // would cost registers.
+    auto scores = [&](const Keys& x, f32x4 (&acc)[NT][2]) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if constexpr (FMT == kINT4) {
-            kf[u][kk] = int4_run(x.k[u][0][kk]);
-          } else {
-            kf[u][kk] = fp8_run(x.k[u][kk >> 1][2 * (kk & 1)], x.k[u][kk >> 1][2 * (kk & 1) + 1]);
+        for (int h = 0; h < HP; ++h) {
+          h8 kf[4];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (FMT == kINT4)
+              kf[kk] = int4_run(x.k[h][u][0][kk]);
+            else
+              kf[kk] = fp8_run(x.k[h][u][(kk >> 1) % W][2 * (kk & 1)],
+                               x.k[h][u][(kk >> 1) % W][2 * (kk & 1) + 1]);
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+              for (int qp = QP - 1; qp >= 0; --qp) {
+                const h8 q = kLowInLds && qp > 0 ? low[(n * 4 + kk) * kWave]
+                                                 : qf[n][kLowInLds ? 0 : qp][kk];
+                a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[kk], q, a, 0, 0, 0);
+              }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[n][u][i] = h == 0 ? a[i] : (c >= 8 ? a[i] : acc[n][u][i]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
+    };
+
+    uint32_t v[HP][8][W];
+    Keys x;
+    Place next;
+    int t = t0 + phase;
+    if (t < last) {
+      // Loads set out in the loop's order (keys, next place, values) here too:
+      // the waits count loads in flight, by the worse of both ways in.
+      x = fetch_keys(t, place_of(t));
+      __builtin_amdgcn_sched_barrier(0);
+      next = place_of(t + phases < last ? t + phases : t);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_values(x, v);
+    }
+    for (; t < last; t += phases) {
+      // the tile after this one; the last one once more, to no use, keeps the
+      // loads in flight countable
+      const int after = t + phases < last ? t + phases : t;
+      // wave-uniform
+      const bool part = x.live != 0xFFFFFFFFu || sees_least < kTileTokens ||
+                        t * kTileTokens > sees_least - kTileTokens;
+      const uint32_t live = x.live;
+      const uint32_t mine = live >> (8 * g);      // of this lane's 8 tokens
+      const int delta = x.delta;
+      // scales through LDS: lane's token -> the 8 tokens of its group;
+      // those of tokens that do not exist become 0
+      wave_lds_fence();
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        const float sc = (live >> (lane & 31)) & 1
+                             ? f16_bits_to_f32(h == 0 ? x.scale & 0xFFFFu : x.scale >> 16) : 0.0f;
+        area.scale[lane >> 5][h][lane & 31] = sc * (lane < 32 ? p.scale_log2 : kWeightScale);
+      }
+      wave_lds_fence();
       f32x4 acc[NT][2];
       if constexpr (QP > 1) {
         // one pass per distance among the tile's tokens
-        uint32_t left = x.live;
+        uint32_t left = live;
         bool first = true;
         do {
           const int lead = left ? __builtin_ctz(left) : 0;
-          const int d = __builtin_amdgcn_readlane(x.delta, TM == kWhole ? 0 : lead);
+          const int d = __builtin_amdgcn_readlane(delta, TM == kWhole ? 0 : lead);
           const uint32_t same = TM == kWhole ? left
-                                             : static_cast<uint32_t>(__ballot(x.delta == d)) & left;
-          if (!loaded || d != turned_by) load_queries(d);
-          loaded = true;
+                                             : static_cast<uint32_t>(__ballot(delta == d)) & left;
+          if (d != turned_by) turn_queries(d);
           turned_by = d;
           f32x4 more[NT][2];
-          scores(kf, more);
+          scores(x, more);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const bool take = first || ((same >> (8 * g + 4 * u + i)) & 1);
+              const bool take = first || (((same >> (8 * g)) >> (4 * u + i)) & 1);
 #pragma unroll
               for (int n = 0; n < NT; ++n) acc[n][u][i] = take ? more[n][u][i] : acc[n][u][i];
             }
@@ -583,14 +629,19 @@ void attend_rows_kernel(AttendParams p) {
           first = false;
         } while (left);
       } else {
-        scores(kf, acc);
+        scores(x, acc);
       }
 
+      // the next tile's keys set out as soon as this one's registers are free,
+      // its values once this tile's are used
+      x = fetch_keys(after, next);
+      __builtin_amdgcn_sched_barrier(0);
+      next = place_of(after + phases < last ? after + phases : after);
       float ks[8], vs[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(&area.scale[0][8 * g + 4 * h]);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(&area.scale[1][8 * g + 4 * h]);
+        const f32x4 a = *reinterpret_cast<const f32x4*>(&area.scale[0][HP == 2 ? c >> 3 : 0][8 * g + 4 * h]);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(&area.scale[1][HP == 2 ? c >> 3 : 0][8 * g + 4 * h]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           ks[4 * h + i] = a[i];
@@ -622,7 +673,7 @@ void attend_rows_kernel(AttendParams p) {
         if (part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const bool vis = ((x.live >> (8 * g + i)) & 1) && static_cast<uint32_t>(t * kTileTokens + 8 * g + i) <
+            const bool vis = ((mine >> i) & 1) && static_cast<uint32_t>(t * kTileTokens + 8 * g + i) <
                                                                      static_cast<uint32_t>(sees[n]);
             sv[n][i] = vis ? sv[n][i] : -INFINITY;
           }
@@ -673,22 +724,58 @@ void attend_rows_kernel(AttendParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) split(w[n][i], n, i);
       }
-      if (FMT == kFP8 && x.live != 0xFFFFFFFFu) {
+      if (FMT == kFP8 && live != 0xFFFFFFFFu) {
         // codes of tokens that do not exist may be NaN
 #pragma unroll
         for (int k = 0; k < 8; ++k)
 #pragma unroll
-          for (int d = 0; d < W; ++d) x.v[k][d] = (x.live >> (8 * g + k)) & 1 ? x.v[k][d] : 0u;
+          for (int h = 0; h < HP; ++h)
+#pragma unroll
+            for (int d = 0; d < W; ++d) v[h][k][d] = (mine >> k) & 1 ? v[h][k][d] : 0u;
       }
-      h8 vf[8];
-      transpose_run<FMT, W>(x.v, vf);
+      // a head's values meet its own rows' weights, 0 in the other's columns
+      auto own = [&](const h8& w8, int h) __attribute__((always_inline)) {
+        if constexpr (HP == 1) return w8;
+        const u32x4 y = __builtin_bit_cast(u32x4, w8);
+        u32x4 z;
 #pragma unroll
-      for (int d = 0; d < 8; ++d)
+        for (int i = 0; i < 4; ++i) z[i] = (c >= 8) == (h == 1) ? y[i] : 0u;
+        return __builtin_bit_cast(h8, z);
+      };
+      // O^T += V^T P^T, four dim tiles at a time; or of weights
+      // that were scaled up
+      auto output = [&](float unscale, bool scaled) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int pp = PP - 1; pp >= 0; --pp)
-            st.o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pf[n][pp], st.o[n][d], 0, 0, 0);
+          for (int h = 0; h < HP; ++h) {
+            h8 vf[4];
+            if (half == 0)
+              transpose_run<FMT, 0, W>(v[h], vf);
+            else
+              transpose_run<FMT, 1, W>(v[h], vf);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int pp = PP - 1; pp >= 0; --pp) {
+                const h8 w8 = own(pf[n][pp], h);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                  f32x4& o = st.o[n][4 * half + d];
+                  if (!scaled) {
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], w8, o, 0, 0, 0);
+                  } else {
+                    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const f32x4 add = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], w8, zero, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(add[i], unscale, o[i]);
+                  }
+                }
+              }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      };
+      output(1.0f, false);
       if (__any(small)) {
         float unscale = 1.0f;
         for (int pass = 0; pass < 5; ++pass) {
@@ -708,40 +795,10 @@ void attend_rows_kernel(AttendParams p) {
               w[n][i] = fabsf(w[n][i]) < kSmall ? rest * 0x1p28f : 0.0f;
               split(w[n][i], n, i);
             }
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              f32x4 add = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int pp = PP - 1; pp >= 0; --pp)
-                add = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d], pf[n][pp], add, 0, 0, 0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                st.o[n][d][i] = __builtin_fmaf(add[i], unscale, st.o[n][d][i]);
-            }
+          output(unscale, true);
         }
       }
-    };
-
-    int t = t0 + phase;
-    if (t < last) {
-      Place here = place_of(t);
-      Place next = t + phases < last ? place_of(t + phases) : here;
-      Raw raw = fetch(t, here);
-      while (true) {
-        const int t_next = t + phases;
-        const bool more = t_next < last;
-        Raw ahead = raw;
-        if (more) {
-          ahead = fetch(t_next, next);
-          if (t_next + phases < last) next = place_of(t_next + phases);
-        }
-        compute(t, raw);
-        if (!more) break;
-        raw = ahead;
-        t = t_next;
-      }
+      fetch_values(x, v);
     }
 
     // Phases join in halves, in a fixed order.
@@ -777,15 +834,16 @@ void attend_rows_kernel(AttendParams p) {
             float x[8];
 #pragma unroll
             for (int d = 0; d < 8; ++d) x[d] = empty ? 0.0f : st.o[n][d][i] * inv;
-            store8_any(p.dtype, dst + (32 * g + 8 * i) * p.elem, x);
+            store8<DT>(dst + (32 * g + 8 * i) * ES, x);
           }
           if (p.lse && g == 0)
             p.lse[static_cast<int64_t>(query[n]) * p.q_heads + head[n]] =
                 log_sum(st.m[n], l);
         } else {
           const int64_t which = at == first_at ? 0 : 1;
-          const int64_t row = (((static_cast<int64_t>(range) * 2 + which) * p.head_sets + set) *
-                                   p.set_heads + sub) * p.part_rows + 16 * n + c;
+          const int64_t row = ((static_cast<int64_t>(range) * 2 + which) * p.n_heads +
+                               (HP == 2 ? kh0 + (c >> 3) : kh0)) * p.part_rows +
+                              16 * n + (HP == 2 ? c & 7 : c);
           float* dst = p.part_o + row * kHeadDim;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -798,11 +856,12 @@ void attend_rows_kernel(AttendParams p) {
         }
       }
     }
-    at += p.ranges > 0 ? static_cast<uint64_t>(t1 - t0) : stride;
+    at += t1 - t0;
+    if (p.ranges == 0) item += gridDim.x / p.head_sets;
   }
 }
 
-template <int FMT, int NT, int QP, int PP>
+template <int FMT, int DT, int HP, int NT, int QP>
 hipError_t launch_rows_tiles(const AttendParams& p, dim3 grid, size_t bytes, hipStream_t stream) {
   auto go = [&](auto* kernel) {
     // more than 64 KB of LDS has to be asked for
@@ -815,20 +874,36 @@ hipError_t launch_rows_tiles(const AttendParams& p, dim3 grid, size_t bytes, hip
     hipLaunchKernelGGL(kernel, grid, dim3(kRowsThreads), bytes, stream, p);
     return hipGetLastError();
   };
-  if (p.block_tokens % kTileTokens == 0) return go(attend_rows_kernel<FMT, NT, QP, PP, kWhole>);
-  if (p.block_tokens % 8 == 0) return go(attend_rows_kernel<FMT, NT, QP, PP, kEighths>);
-  return go(attend_rows_kernel<FMT, NT, QP, PP, kAny>);
+  if (p.block_tokens % kTileTokens == 0) return go(attend_rows_kernel<FMT, DT, HP, NT, QP, kWhole>);
+  if (p.block_tokens % 8 == 0) return go(attend_rows_kernel<FMT, DT, HP, NT, QP, kEighths>);
+  return go(attend_rows_kernel<FMT, DT, HP, NT, QP, kAny>);
+}
+
+// hp, nt: two heads per score tile, or 16 nt rows of one.
+template <int FMT, int DT>
+hipError_t launch_rows_dtype(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
+                             hipStream_t stream) {
+  if (DT == kF32 || p.delta) {
+    if (hp == 2) return launch_rows_tiles<FMT, DT, 2, 1, 2>(p, grid, bytes, stream);
+    if (nt == 1) return launch_rows_tiles<FMT, DT, 1, 1, 2>(p, grid, bytes, stream);
+  }
+  if constexpr (DT != kF32) {
+    if (p.delta) return launch_rows_tiles<FMT, DT, 1, 2, 2>(p, grid, bytes, stream);
+    if (hp == 2) return launch_rows_tiles<FMT, DT, 2, 1, 1>(p, grid, bytes, stream);
+    return nt == 1 ? launch_rows_tiles<FMT, DT, 1, 1, 1>(p, grid, bytes, stream)
+                   : launch_rows_tiles<FMT, DT, 1, 2, 1>(p, grid, bytes, stream);
+  }
+  return hipErrorInvalidValue;           // not reached: 32 rows of fp32 are never asked for
 }
 
 template <int FMT>
-hipError_t launch_rows_format(const AttendParams& p, int nt, dim3 grid, size_t bytes,
+hipError_t launch_rows_format(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                               hipStream_t stream) {
-  if (p.dtype == kF32) return launch_rows_tiles<FMT, 1, 2, 2>(p, grid, bytes, stream);
-  if (p.delta)
-    return nt == 1 ? launch_rows_tiles<FMT, 1, 2, 1>(p, grid, bytes, stream)
-                   : launch_rows_tiles<FMT, 2, 2, 1>(p, grid, bytes, stream);
-  return nt == 1 ? launch_rows_tiles<FMT, 1, 1, 1>(p, grid, bytes, stream)
-                 : launch_rows_tiles<FMT, 2, 1, 1>(p, grid, bytes, stream);
+  switch (p.dtype) {
+    case kF32: return launch_rows_dtype<FMT, kF32>(p, hp, nt, grid, bytes, stream);
+    case kF16: return launch_rows_dtype<FMT, kF16>(p, hp, nt, grid, bytes, stream);
+    default: return launch_rows_dtype<FMT, kBF16>(p, hp, nt, grid, bytes, stream);
+  }
 }
 
 }  // namespace hkv

@@ -3,9 +3,9 @@
 
 namespace hkv {
 
-hipError_t launch_rows_fp8(const AttendParams& p, int nt, dim3 grid, size_t bytes,
+hipError_t launch_rows_fp8(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                             hipStream_t stream) {
-  return launch_rows_format<kFP8>(p, nt, grid, bytes, stream);
+  return launch_rows_format<kFP8>(p, hp, nt, grid, bytes, stream);
 }
 
 }  // namespace hkv

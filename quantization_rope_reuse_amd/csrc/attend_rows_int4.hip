@@ -3,9 +3,9 @@
 
 namespace hkv {
 
-hipError_t launch_rows_int4(const AttendParams& p, int nt, dim3 grid, size_t bytes,
+hipError_t launch_rows_int4(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                             hipStream_t stream) {
-  return launch_rows_format<kINT4>(p, nt, grid, bytes, stream);
+  return launch_rows_format<kINT4>(p, hp, nt, grid, bytes, stream);
 }
 
 }  // namespace hkv
