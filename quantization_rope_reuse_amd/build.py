@@ -1,4 +1,5 @@
-"""Build libhkv.so (HIP, gfx950) in place, next to this file.
+"""Build libhkv.so (HIP, gfx950) and the native part of the binding in place,
+next to this file.
 
     python -m quantization_rope_reuse_amd.build
 
@@ -67,12 +68,30 @@ def build(verbose: bool = False) -> str:
         objs.append(obj)
         jobs.append([cc, *compile_flags(), "-c", os.path.join(CSRC, src), "-o", obj])
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
-        for f in [ex.submit(_run, j, verbose) for j in jobs]:
+        for f in [*(ex.submit(_run, j, verbose) for j in jobs), ex.submit(build_native, verbose)]:
             f.result()
     tmp = LIB + ".tmp"
     _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_native(verbose: bool = False) -> str:
+    """The native part of the Python binding (host code only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import TORCH_LIB_PATH, include_paths
+    out = os.path.join(PKG, "_native.so")
+    tmp = out + ".tmp"
+    flags = [f"-I{d}" for d in (*include_paths(), "/opt/rocm/include", INCLUDE,
+                                sysconfig.get_paths()["include"])]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+          "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *flags,
+          os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{TORCH_LIB_PATH}", "-ltorch_python",
+          "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"], verbose)
+    os.replace(tmp, out)
+    return out
 
 
 def build_test_kernels(verbose: bool = False) -> list:

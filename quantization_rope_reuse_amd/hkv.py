@@ -1,12 +1,13 @@
-"""Thin ctypes binding of libhkv (include/hkv.h, include/hkv_serve.h).
+"""Thin binding of libhkv (include/hkv.h, include/hkv_serve.h): ctypes, and
+csrc/binding.cpp for the fetch and the serving calls.
 
 Argument marshalling only: every step of put, CRC and fetch runs in the HIP
 kernels of libhkv.so.  torch is used for device memory and streams: tensors
 supply device pointers and strides, and calls are enqueued on the caller's
 current torch stream unless another is given.
 
-There is no fallback: if libhkv.so is missing or cannot be loaded, importing
-the library raises.
+There is no fallback: if libhkv.so or the native part is missing or cannot be
+loaded, the calls raise.
 """
 
 from __future__ import annotations
@@ -102,6 +103,7 @@ class KeyShift(ctypes.Structure):
 
 
 _lib = None
+_native = _native_of = None
 
 
 def declared_symbols():
@@ -202,6 +204,25 @@ def lib():
         l.hkv_status_string.restype = ctypes.c_char_p
         _lib = l
     return _lib
+
+
+# The library's calls that binding.cpp makes.
+NATIVE_CALLS = ("hkv_plan_step", "hkv_rope_heads", "hkv_append_tokens", "hkv_attend_records",
+                "hkv_attend_workspace_bytes", "hkv_fetch_dequant_rope_shift",
+                "hkv_fetch_dequant_rope_shift_tokens", "hkv_record_bytes")
+
+
+def native():
+    """The native part of the binding (csrc/binding.cpp), calling this
+    module's library: tensor checks and structures of calls that take the GPU
+    a few microseconds, which they would take this module longer."""
+    global _native, _native_of
+    l = lib()
+    if _native is None or _native_of is not l:
+        from . import _native as module
+        module.bind({n: ctypes.cast(getattr(l, n), ctypes.c_void_p).value for n in NATIVE_CALLS})
+        _native, _native_of = module, l
+    return _native
 
 
 def status_string(status: int) -> str:
@@ -412,44 +433,25 @@ def noalloc_scratch_bytes() -> int:
     return NOALLOC_SCRATCH_BYTES
 
 
-def _fetch(name, records, fmt, block_table, delta, n_delta, rope_base, pairs, k_pages, v_pages,
-           visit_order, stream):
-    pages, shp, dt = _pages(k_pages, v_pages)
-    L, _, tb, H, d = shp
-    nb = block_table.numel()
-    if records.shape[0] != L or records.shape[1] != nb or delta.numel() != n_delta(nb, tb):
-        raise ValueError("records [L, n_blocks, bytes], table and deltas must agree")
-    if visit_order is not None and visit_order.numel() != nb:
-        raise ValueError("visit_order must hold n_blocks entries")
-    shape = Shape(L, nb, tb, H, d)
-    rec = _records(records, fmt, tb, H)
-    order = None if visit_order is None else _i32(visit_order, "visit_order")
-    st = getattr(lib(), name)(
-        ctypes.byref(shape), FORMATS[fmt], ctypes.byref(rec), _i32(block_table, "block_table"),
-        _i32(delta, "delta_m"), order, float(rope_base), PAIRS[pairs], ctypes.byref(pages),
-        dt, _stream(stream, k_pages.device))
-    _check(name, st)
-    return k_pages, v_pages
-
-
-@_on_one_gpu
 def fetch_dequant_rope_shift(records, fmt, block_table, delta_m, rope_base, pairs,
                              k_pages, v_pages, visit_order=None, stream=None):
     """Dequantize records[:, b], shift keys by delta_m[b], store at page
     block_table[b] of k/v_pages (dtype of the pages).  visit_order: optional
     int32 permutation of the blocks (see page_visit_order)."""
-    return _fetch("hkv_fetch_dequant_rope_shift", records, fmt, block_table, delta_m,
-                  lambda nb, tb: nb, rope_base, pairs, k_pages, v_pages, visit_order, stream)
+    st = native().fetch(False, records, FORMATS[fmt], block_table, delta_m, rope_base,
+                        PAIRS[pairs], k_pages, v_pages, visit_order, stream)
+    _check("hkv_fetch_dequant_rope_shift", st)
+    return k_pages, v_pages
 
 
-@_on_one_gpu
 def fetch_dequant_rope_shift_tokens(records, fmt, block_table, delta_m_tokens, rope_base, pairs,
                                     k_pages, v_pages, visit_order=None, stream=None):
     """As fetch_dequant_rope_shift with one delta per token: delta_m_tokens
     is an int32 [n_blocks, block_tokens] tensor."""
-    return _fetch("hkv_fetch_dequant_rope_shift_tokens", records, fmt, block_table,
-                  delta_m_tokens, lambda nb, tb: nb * tb, rope_base, pairs, k_pages, v_pages,
-                  visit_order, stream)
+    st = native().fetch(True, records, FORMATS[fmt], block_table, delta_m_tokens, rope_base,
+                        PAIRS[pairs], k_pages, v_pages, visit_order, stream)
+    _check("hkv_fetch_dequant_rope_shift_tokens", st)
+    return k_pages, v_pages
 
 
 def fetch_staged(host_records, fmt, block_table, delta_m, rope_base, pairs, k_pages, v_pages,
@@ -757,41 +759,6 @@ def alloc_plan(n_requests: int, n_tokens: int, device="cuda") -> StepPlan:
                     i32(1))
 
 
-def _table(t: torch.Tensor):
-    """Entries per row and row stride of an int32 [n_requests, max_blocks]
-    tensor; strides that address nothing may be anything."""
-    if t.dim() != 2 or t.dtype != torch.int32 or (
-            t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("block_table must be an int32 [n_requests, max_blocks] tensor, last "
-                         "axis contiguous")
-    return t.shape[1], t.stride(0) if t.shape[0] > 1 and t.numel() > 0 else t.shape[1]
-
-
-@_on_one_gpu
-def _plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, out_kv_len, q_start,
-               positions, slots, refused, out_count, block_tokens, stream):
-    R = kv_len.numel()
-    mb, stride = _table(block_table)
-    if block_table.shape[0] != R or new_tokens.numel() != R or out_kv_len.numel() != R \
-            or refused.numel() != R or q_start.numel() != R + 1:
-        raise ValueError("kv_len, new_tokens, block_table, refused [n_requests] and q_start "
-                         "[n_requests + 1] must agree")
-    if free_count.numel() != 1 or out_count.numel() != 1:
-        raise ValueError("free_count must hold one element")
-    if slots.dtype != torch.int64 or not slots.is_contiguous() or \
-            slots.numel() != positions.numel():
-        raise ValueError("slots must be a contiguous int64 tensor as long as positions")
-    step = Step(R, int(block_tokens), mb, positions.numel(), _i32(kv_len, "kv_len"),
-                _i32(new_tokens, "new_tokens"), block_table.data_ptr(), stride,
-                _i32(free_blocks, "free_blocks"), free_blocks.numel(),
-                _i32(free_count, "free_count"), _i32(out_count, "free_count"),
-                _i32(out_kv_len, "kv_len"), _i32(q_start, "q_start"),
-                _i32(positions, "positions"), ctypes.c_void_p(slots.data_ptr()),
-                _i32(refused, "refused"))
-    _check("hkv_plan_step", lib().hkv_plan_step(ctypes.byref(step),
-                                                _stream(stream, kv_len.device)))
-
-
 def plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, block_tokens: int,
               n_tokens: int, out=None, stream=None) -> StepPlan:
     """The plan of one step from its request lengths: table entries for the
@@ -802,25 +769,10 @@ def plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, block_to
     in refused and keeps its length.  kv_len, new_tokens, free_count: int32
     on the GPU; free_count of the result is the next step's.  out: a StepPlan
     of tensors to write (alloc_plan), none of them an input."""
-    if out is None:
-        out = alloc_plan(kv_len.numel(), int(n_tokens), device=kv_len.device)
-    if out.positions.numel() != n_tokens:
-        raise ValueError("out must hold n_tokens positions")
-    _plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, *out[:5],
-               out.free_count, block_tokens, stream)
-    return out
-
-
-def _heads(t: torch.Tensor, name: str):
-    """[n_tokens, n_heads, 128] rows of head vectors."""
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
-        raise ValueError(f"{name} must be a [n_tokens, n_heads, {HEAD_DIM}] tensor, last axis "
-                         "contiguous")
-    if t.dtype not in TORCH_DTYPES:
-        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
-    # the stride of an axis of one entry addresses nothing and may be anything
-    return Heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0,
-                 t.stride(1) if t.shape[1] > 1 else 0, t.shape[1])
+    st, *plan = native().plan_step(kv_len, new_tokens, block_table, free_blocks, free_count,
+                                   block_tokens, n_tokens, out, stream)
+    _check("hkv_plan_step", st)
+    return StepPlan(*plan) if out is None else out
 
 
 @functools.lru_cache(maxsize=64)
@@ -853,7 +805,12 @@ def rope_axes(rope_base: float, pairs, sections=(HEAD_DIM // 2,), order="blocked
                     (ctypes.c_int8 * half)(*axis), (ctypes.c_uint8 * half)(*freq))
 
 
-@_on_one_gpu
+@functools.lru_cache(maxsize=64)
+def _axes_address(*args):
+    axes = rope_axes(*args)
+    return ctypes.addressof(axes), axes          # the structure lives as long as the entry
+
+
 def rope_heads(q, k, positions, rope_base: float, pairs, sections=(HEAD_DIM // 2,),
                order="blocked", freq=None, inverse: bool = False, q_out=None, k_out=None,
                stream=None):
@@ -863,59 +820,19 @@ def rope_heads(q, k, positions, rope_base: float, pairs, sections=(HEAD_DIM // 2
     inverse=True turns back: it strips positions, and it is the gradient with
     respect to q and k given that of the results.  q_out, k_out: tensors to
     write, the inputs themselves for a rotation in place."""
-    axes = rope_axes(float(rope_base), pairs, tuple(sections),
-                     order if isinstance(order, str) else tuple(order),
-                     None if freq is None else tuple(freq))
-    n = q.shape[0]
-    pos = positions if positions.dim() == 2 else positions.unsqueeze(0)
-    if pos.dim() != 2 or pos.dtype != torch.int32 or pos.shape != (axes.n_axes, n) or (
-            n > 1 and pos.stride(1) != 1):
-        raise ValueError(f"positions must be int32 [{axes.n_axes}, n_tokens], last axis contiguous")
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    heads = [_heads(q, "q"), Heads(), _heads(q_out, "q_out"), Heads()]
-    same = q_out.shape == q.shape and q_out.dtype == q.dtype
-    if k is not None:
-        heads[1], heads[3] = _heads(k, "k"), _heads(k_out, "k_out")
-        same = same and k.shape[0] == n and k_out.shape == k.shape and \
-            k.dtype == k_out.dtype == q.dtype
-    if not same:
-        raise ValueError("q, k and their outputs must share dtype and n_tokens, each output its "
-                         "input's shape")
-    st = lib().hkv_rope_heads(ctypes.byref(axes), ctypes.c_void_p(pos.data_ptr()),
-                              pos.stride(0) if axes.n_axes > 1 else 0, n,
-                              *(ctypes.byref(h) for h in heads), TORCH_DTYPES[q.dtype],
-                              1 if inverse else 0, _stream(stream, q.device))
+    axes = _axes_address(float(rope_base), pairs, tuple(sections),
+                         order if isinstance(order, str) else tuple(order),
+                         None if freq is None else tuple(freq))
+    st, q_out, k_made = native().rope_heads(q, k, positions, axes[0], inverse, q_out, k_out, stream)
     _check("hkv_rope_heads", st)
-    return q_out, k_out
+    return q_out, k_made
 
 
-def _pool(records, fmt, block_tokens, n_kv_heads):
-    """One layer's records [n_blocks, bytes] (or [1, n_blocks, bytes])."""
-    r = records if records.dim() == 3 else records.unsqueeze(0)
-    if r.dim() != 3 or r.shape[0] != 1:
-        raise ValueError("records must be one layer's uint8 [n_blocks, bytes] tensor")
-    return (Shape(1, r.shape[1], block_tokens, n_kv_heads, HEAD_DIM),
-            _records(r, fmt, block_tokens, n_kv_heads))
-
-
-@_on_one_gpu
 def append_tokens(k, v, slots, records, fmt, block_tokens: int, stream=None):
     """Quantize the new tokens' keys and values, [n_tokens, n_kv_heads, 128]
     each, into slots (int64 [n_tokens]; block * block_tokens + token, negative
     to skip) of one layer's records [n_blocks, bytes]."""
-    if k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError("k and v must share shape and dtype")
-    kh, vh = _heads(k, "k"), _heads(v, "v")
-    if slots.dtype != torch.int64 or not slots.is_contiguous() or slots.numel() != k.shape[0]:
-        raise ValueError("slots must be a contiguous int64 tensor of n_tokens elements")
-    shape, rec = _pool(records, fmt, block_tokens, k.shape[1])
-    st = lib().hkv_append_tokens(ctypes.byref(shape), FORMATS[fmt], ctypes.byref(kh),
-                                 ctypes.byref(vh), TORCH_DTYPES[k.dtype], k.shape[0],
-                                 ctypes.c_void_p(slots.data_ptr()), ctypes.byref(rec),
-                                 _stream(stream, k.device))
+    st = native().append_tokens(k, v, slots, records, FORMATS[fmt], block_tokens, stream)
     _check("hkv_append_tokens", st)
     return records
 
@@ -929,7 +846,6 @@ def attend_workspace_bytes(n_blocks: int, block_tokens: int, n_kv_heads: int, n_
                                                 n_q_heads, TORCH_DTYPES[dtype]))
 
 
-@_on_one_gpu
 def attend_records(q, records, fmt, block_tokens: int, n_kv_heads: int, block_table, kv_len,
                    q_start=None, max_queries=None, sm_scale=None, causal: bool = True,
                    delta_m=None, rope_base: float = 10000.0, pairs="half_split", out=None,
@@ -945,47 +861,10 @@ def attend_records(q, records, fmt, block_tokens: int, n_kv_heads: int, block_ta
     as fetch_dequant_rope_shift does (rope_base, pairs).  workspace: True
     (allocated here if one is needed), or a uint8 tensor of
     attend_workspace_bytes bytes."""
-    heads = _heads(q, "q")
-    n, hq = q.shape[0], q.shape[1]
-    mb, stride = _table(block_table)
-    R = block_table.shape[0]
-    if kv_len.numel() != R or (q_start is not None and q_start.numel() != R + 1) or \
-            (q_start is None and n != R):
-        raise ValueError("kv_len [n_requests], q_start [n_requests + 1] (or one query per "
-                         "request) and block_table must agree")
-    if max_queries is None:
-        max_queries = 1 if q_start is None else max(n, 1)
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and dtype")
-    if lse is None:
-        lse = torch.empty((n, hq), dtype=torch.float32, device=q.device)
-    if lse.shape != (n, hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [n_tokens, n_q_heads] tensor")
-    shift = None
-    if delta_m is not None:
-        if delta_m.shape != block_table.shape or _table(delta_m) != (mb, stride):
-            raise ValueError("delta_m must have block_table's shape, type and strides")
-        shift = ctypes.byref(KeyShift(delta_m.data_ptr(), float(rope_base), PAIRS[pairs]))
-    shape, rec = _pool(records, fmt, block_tokens, n_kv_heads)
-    req = Requests(R, mb, int(max_queries), block_table.data_ptr(), stride,
-                   _i32(kv_len, "kv_len"), None if q_start is None else _i32(q_start, "q_start"))
-    need = lib().hkv_attend_workspace_bytes(ctypes.byref(shape), ctypes.byref(req), n, hq,
-                                            TORCH_DTYPES[q.dtype])
-    if workspace is True:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor")
-        ws_ptr, ws_bytes = ctypes.c_void_p(workspace.data_ptr()), workspace.numel()
-    oh = _heads(out, "out")
-    st = lib().hkv_attend_records(
-        ctypes.byref(shape), FORMATS[fmt], ctypes.byref(rec), ctypes.byref(req),
-        ctypes.byref(heads), TORCH_DTYPES[q.dtype], n,
-        float(HEAD_DIM ** -0.5 if sm_scale is None else sm_scale), 1 if causal else 0, shift,
-        ctypes.byref(oh), ctypes.c_void_p(lse.data_ptr()), ws_ptr, ws_bytes,
-        _stream(stream, q.device))
+    st, out, lse = native().attend_records(
+        q, records, FORMATS[fmt], block_tokens, n_kv_heads, block_table, kv_len, q_start,
+        -1 if max_queries is None else max(int(max_queries), 0),
+        HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, causal, delta_m, rope_base,
+        PAIRS[pairs], out, lse, workspace, stream)
     _check("hkv_attend_records", st)
     return out, lse
