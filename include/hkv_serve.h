@@ -178,7 +178,9 @@ typedef struct {
  * workspace: 16-byte aligned, hkv_attend_workspace_bytes() bytes (0: none
  * needed); its contents before and after do not matter, and calls that share
  * one must not overlap.  The result does not depend on scheduling: the same
- * call gives the same bits. */
+ * call gives the same bits.  n_requests above 65535, n_kv_heads above 4096,
+ * max_blocks * block_tokens or n_tokens * n_heads above 2^31 - 1:
+ * HKV_ERR_UNSUPPORTED. */
 int hkv_attend_records(const hkv_shape* shape, int32_t fmt, const hkv_records* records,
                        const hkv_requests* requests, const hkv_heads* q, int32_t dtype,
                        int32_t n_tokens, double sm_scale, int32_t causal,

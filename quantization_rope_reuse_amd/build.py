@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libhkv.so")
 SOURCES = ("api.hip", "quant.hip", "fetch.hip", "crc.hip", "order.hip", "streams.hip",
            "select.hip", "frames.hip", "probe.hip", "noalloc.hip",
            "staged.hip", "serve_api.hip", "plan.hip", "rope.hip", "append.hip", "attend.hip",
-           "attend_rows_int4.hip", "attend_rows_fp8.hip")
+           "attend_rows_int4.hip", "attend_rows_fp8.hip",
+           "attend_prompt_int4.hip", "attend_prompt_fp8.hip")
 ARCH = "gfx950"
 
 

@@ -2,6 +2,9 @@
 // and the join of partial results.
 #include "attend_rows.h"
 
+#ifndef HKV_PROMPT
+#define HKV_PROMPT 64
+#endif
 namespace hkv {
 namespace {
 
@@ -18,17 +21,28 @@ __global__ __launch_bounds__(kJoinMost * kWave) void attend_join_kernel(AttendPa
   if (j >= min(s.n_q, p.max_queries)) return;
   const int head = blockIdx.x - j * p.q_heads;
   const int kh = head / p.group;
-  const int row = j * p.group + (head - kh * p.group);
-  const int item = row / item_rows;
-  const uint32_t tiles = tiles_of(s);
-  const uint32_t f0 = p.prefix_out[r] + item * tiles;
-  const uint32_t per = p.prefix_out[p.n_requests + 1];
-  const int w0 = f0 / per, w1 = (f0 + tiles - 1) / per;
-  if (w0 == w1) return;
+  // The partial results of this row: w0 .. w1.  The rows kernel's ranges that
+  // an item reaches over (alone, it wrote the result), or the prompt kernel's
+  // cuts.
+  int w0 = 0, w1 = p.splits - 1;
+  uint32_t f0 = 0, per = 0;
+  int64_t in_item = 0;
+  if (p.splits == 0) {
+    const int row = j * p.group + (head - kh * p.group);
+    const int item = row / item_rows;
+    const uint32_t tiles = tiles_of(s);
+    f0 = p.prefix_out[r] + item * tiles;
+    per = p.prefix_out[p.n_requests + 1];
+    w0 = f0 / per;
+    w1 = (f0 + tiles - 1) / per;
+    if (w0 == w1) return;
+    in_item = row - item * item_rows;
+  }
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = threadIdx.x / kWave;
-  const int64_t in_item = row - item * item_rows;
   auto at = [&](int w) {
+    if (p.splits > 0)
+      return (static_cast<int64_t>(w) * p.n_tokens + s.start + j) * p.q_heads + head;
     const int which = w == w0 && f0 > w0 * per ? 1 : 0;
     return (static_cast<int64_t>(w * 2 + which) * p.n_heads + kh) * p.part_rows + in_item;
   };
@@ -90,6 +104,7 @@ __global__ __launch_bounds__(kJoinMost * kWave) void attend_join_kernel(AttendPa
 }
 
 struct Share {
+  int splits;              // > 0: the prompt kernel
   int hp, nt;              // heads per score tile, tiles of 16 rows: 16 nt / hp rows per item
   int set_heads, head_sets, ranges, min_tiles, part_rows;
   int64_t rows;            // partial rows in all
@@ -99,12 +114,28 @@ struct Share {
 // How a call's work is shared out, from the sizes that the host knows.
 Share share_of(int fmt, const Geometry& g, const hkv_requests& req, int32_t n_tokens,
                int32_t n_q_heads, int dtype) {
-  Share s;
+  Share s = {};
   const int64_t queries = req.max_queries < n_tokens ? req.max_queries : n_tokens;
   const int64_t rows = queries * (n_q_heads / g.n_heads);
+  s.splits = 0;
+  if (rows > HKV_PROMPT) {
+    // one workgroup per 256 rows and key head; their tokens are cut where
+    // these are too few for the CUs
+    s.items = (rows + kPromptRows - 1) / kPromptRows;
+    int64_t most = static_cast<int64_t>(n_tokens) * (n_q_heads / g.n_heads) / kPromptRows + req.n_requests;
+    const int64_t all = req.n_requests * s.items;
+    most = (most < all ? most : all) * g.n_heads;
+    const int64_t cuts = 256 / (most < 1 ? 1 : most);
+    const int64_t long_enough = static_cast<int64_t>(req.max_blocks) * g.block_tokens / 512;
+    s.splits = static_cast<int>(cuts < long_enough ? cuts : long_enough);
+    s.splits = s.splits < 1 ? 1 : s.splits;
+    s.hp = s.nt = 1;
+    s.rows = s.splits > 1 ? static_cast<int64_t>(s.splits) * n_tokens * n_q_heads : 0;
+    return s;
+  }
   // Two heads of at most 8 rows share a score tile, which halves the softmax
   // and the bookkeeping of each.
-    s.hp = rows <= 8 && g.n_heads % 2 == 0 ? 2 : 1;
+  s.hp = rows <= 8 && g.n_heads % 2 == 0 ? 2 : 1;
   s.nt = dtype == kF32 || rows <= 16 ? 1 : 2;
   const int64_t item_rows = 16 * s.nt / s.hp;
   s.items = (rows + item_rows - 1) / item_rows;
@@ -134,7 +165,7 @@ int64_t prefix_bytes(const hkv_requests& req) {
 }
 
 int64_t share_bytes(const Share& s, const hkv_requests& req) {
-  return s.ranges > 0 ? prefix_bytes(req) + (s.rows * 8 + 15) / 16 * 16 + s.rows * kHeadDim * 4 : 0;
+  return s.rows > 0 ? prefix_bytes(req) + (s.rows * 8 + 15) / 16 * 16 + s.rows * kHeadDim * 4 : 0;
 }
 
 }  // namespace
@@ -190,6 +221,7 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     p.theta[i] = c.delta ? quarter_turns(c.rope_base, i) : 0.0;
 
   const Share share = share_of(c.fmt, c.g, c.req, c.n_tokens, c.q.n_heads, c.dtype);
+  p.splits = share.splits;
   p.set_heads = share.set_heads;
   p.head_sets = share.head_sets;
   p.ranges = share.ranges;
@@ -198,31 +230,39 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
   p.prefix_out = nullptr;
   p.part_ml = nullptr;
   p.part_o = nullptr;
-  // the join of the waves needs more than 32 rows' second query parts
-  size_t bytes = kRowsWaves * kWaveAreaBytes + (kRowsWaves / 2) * share.nt * (8192 + 512);
-  dim3 grid;
-  if (share.ranges > 0) {
+  if (share.rows > 0) {
     char* ws = static_cast<char*>(c.workspace);
     p.prefix_out = reinterpret_cast<uint32_t*>(ws);
     ws += prefix_bytes(c.req);
     p.part_ml = reinterpret_cast<float*>(ws);
     p.part_o = reinterpret_cast<float*>(ws + (share.rows * 8 + 15) / 16 * 16);
-    bytes += static_cast<size_t>(prefix_bytes(c.req));
-    grid = dim3(static_cast<unsigned>(share.ranges * share.head_sets));
-  } else {
-    // items beyond 65,535 sets of workgroups are taken in turn
-    int64_t x = share.items;
-    const int64_t most = 65535 / share.head_sets;
-    x = x < most ? x : most;
-    x = x < 1 ? 1 : x;
-    grid = dim3(static_cast<unsigned>(x * share.head_sets), static_cast<unsigned>(c.req.n_requests));
   }
-  const hipError_t e = c.fmt == kFP8 ? launch_rows_fp8(p, share.hp, share.nt, grid, bytes, stream)
-                                     : launch_rows_int4(p, share.hp, share.nt, grid, bytes, stream);
-  if (e != hipSuccess || share.ranges == 0) return e;
+  // items beyond 65,535 workgroups per request are taken in turn
+  auto per_request = [&](int64_t sets) {
+    const int64_t most = 65535 / sets;
+    int64_t x = share.items < most ? share.items : most;
+    x = x < 1 ? 1 : x;
+    return dim3(static_cast<unsigned>(x * sets), static_cast<unsigned>(c.req.n_requests));
+  };
+  hipError_t e;
+  if (share.splits > 0) {
+    const dim3 grid = per_request(static_cast<int64_t>(c.g.n_heads) * share.splits);
+    e = c.fmt == kFP8 ? launch_prompt_fp8(p, grid, stream) : launch_prompt_int4(p, grid, stream);
+  } else {
+    // the join of the waves needs more than 32 rows' second query parts
+    size_t bytes = kRowsWaves * kWaveAreaBytes + (kRowsWaves / 2) * share.nt * (8192 + 512);
+    if (share.ranges > 0) bytes += static_cast<size_t>(prefix_bytes(c.req));
+    const dim3 grid = share.ranges > 0 ? dim3(static_cast<unsigned>(share.ranges * share.head_sets))
+                                       : per_request(share.head_sets);
+    e = c.fmt == kFP8 ? launch_rows_fp8(p, share.hp, share.nt, grid, bytes, stream)
+                      : launch_rows_int4(p, share.hp, share.nt, grid, bytes, stream);
+  }
+  if (e != hipSuccess || share.rows == 0) return e;
   const int64_t queries = c.req.max_queries < c.n_tokens ? c.req.max_queries : c.n_tokens;
   // about 8 partial results of a row for each wave
-  const int64_t parts = share.ranges / (static_cast<int64_t>(c.req.n_requests) * share.items);
+  const int64_t parts = share.splits > 0
+                            ? share.splits
+                            : share.ranges / (static_cast<int64_t>(c.req.n_requests) * share.items);
   int waves = 1;
   while (waves < kJoinMost && waves * 8 < parts) waves *= 2;
   hipLaunchKernelGGL(attend_join_kernel,

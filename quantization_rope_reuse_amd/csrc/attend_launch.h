@@ -11,6 +11,10 @@ constexpr int kRowsThreads = kRowsWaves * 64;
 constexpr int kMaxFlatRequests = 1024; // requests whose tiles are dealt out evenly
 constexpr int kWaveAreaBytes = 1280;   // LDS of a wave of the rows kernel
 
+constexpr int kPromptWaves = 8;
+constexpr int kPromptThreads = kPromptWaves * 64;
+constexpr int kPromptRows = kPromptWaves * 32;   // rows of a workgroup of the prompt kernel
+
 struct AttendParams {
   const uint8_t* rec;
   int64_t rec_block;
@@ -40,6 +44,7 @@ struct AttendParams {
   int32_t ranges;          // > 0: all tiles dealt out over this many ranges
   int32_t min_tiles;       // least tiles of a range
   int32_t part_rows;       // rows per head of a partial result
+  int32_t splits;          // the prompt kernel's cuts of the tokens; 0: the rows kernel runs
   uint32_t* prefix_out;    // [n_requests + 2]: first tile of each request, total, tiles per range
   float* part_ml;          // reference and sum of each partial row
   float* part_o;           // its weighted values
@@ -50,5 +55,7 @@ hipError_t launch_rows_int4(const AttendParams& p, int hp, int nt, dim3 grid, si
                             hipStream_t stream);
 hipError_t launch_rows_fp8(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                            hipStream_t stream);
+hipError_t launch_prompt_int4(const AttendParams& p, dim3 grid, hipStream_t stream);
+hipError_t launch_prompt_fp8(const AttendParams& p, dim3 grid, hipStream_t stream);
 
 }  // namespace hkv

@@ -185,7 +185,7 @@ __device__ __forceinline__ void merge_rows(RowState<NT>& a, const f32x4* o, cons
 enum TileMode { kWhole = 0, kEighths = 1, kAny = 2 };
 
 template <int FMT, int DT, int HP, int NT, int QP, int TM>
-__global__ __launch_bounds__(kRowsThreads, 2)
+__global__ __launch_bounds__(kRowsThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void attend_rows_kernel(AttendParams p) {
   constexpr int CB = FMT == kFP8 ? kHeadDim : kHeadDim / 2;
   constexpr int W = CB / 64;                  // dwords per 8 codes

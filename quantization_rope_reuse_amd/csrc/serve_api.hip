@@ -61,6 +61,7 @@ int check_requests(const hkv_requests* r, const Geometry& g, int32_t n_tokens, i
     return HKV_ERR_INVALID_ARG;
   if (n_q_heads < 1 || n_q_heads % g.n_heads != 0) return HKV_ERR_INVALID_ARG;
   if (r->n_requests > 65535) return HKV_ERR_UNSUPPORTED;                 // grid.y limit
+  if (g.n_heads > 4096) return HKV_ERR_UNSUPPORTED;                      // grid.x limit
   if (static_cast<int64_t>(r->max_blocks) * g.block_tokens > INT32_MAX) return HKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(n_tokens) * n_q_heads > INT32_MAX) return HKV_ERR_UNSUPPORTED;
   if (!hkv::span_ok({{r->n_requests, r->table_stride}}, r->max_blocks)) return HKV_ERR_INVALID_ARG;
