@@ -112,7 +112,7 @@ struct Share {
 };
 
 // How a call's work is shared out, from the sizes that the host knows.
-Share share_of(int fmt, const Geometry& g, const hkv_requests& req, int32_t n_tokens,
+Share share_of(int fmt, bool moved, const Geometry& g, const hkv_requests& req, int32_t n_tokens,
                int32_t n_q_heads, int dtype) {
   Share s = {};
   const int64_t queries = req.max_queries < n_tokens ? req.max_queries : n_tokens;
@@ -136,7 +136,7 @@ Share share_of(int fmt, const Geometry& g, const hkv_requests& req, int32_t n_to
   // Two heads of at most 8 rows share a score tile, which halves the softmax
   // and the bookkeeping of each.
   s.hp = rows <= 8 && g.n_heads % 2 == 0 ? 2 : 1;
-  s.nt = dtype == kF32 || rows <= 16 ? 1 : 2;
+  s.nt = dtype == kF32 || moved || rows <= 16 ? 1 : 2;
   const int64_t item_rows = 16 * s.nt / s.hp;
   s.items = (rows + item_rows - 1) / item_rows;
   const int64_t max_len = static_cast<int64_t>(req.max_blocks) * g.block_tokens;
@@ -173,10 +173,11 @@ int64_t share_bytes(const Share& s, const hkv_requests& req) {
 int64_t attend_workspace_bytes(const Geometry& g, const hkv_requests& req, int32_t n_tokens,
                                int32_t n_q_heads, int dtype) {
   int64_t most = 0;
-  for (int fmt : {kFP8, kINT4}) {
-    const int64_t b = share_bytes(share_of(fmt, g, req, n_tokens, n_q_heads, dtype), req);
-    most = b > most ? b : most;
-  }
+  for (int fmt : {kFP8, kINT4})
+    for (bool moved : {false, true}) {
+      const int64_t b = share_bytes(share_of(fmt, moved, g, req, n_tokens, n_q_heads, dtype), req);
+      most = b > most ? b : most;
+    }
   return most;
 }
 
@@ -220,7 +221,7 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
   for (int i = 0; i < kHeadDim / 2; ++i)
     p.theta[i] = c.delta ? quarter_turns(c.rope_base, i) : 0.0;
 
-  const Share share = share_of(c.fmt, c.g, c.req, c.n_tokens, c.q.n_heads, c.dtype);
+  const Share share = share_of(c.fmt, c.delta != nullptr, c.g, c.req, c.n_tokens, c.q.n_heads, c.dtype);
   p.splits = share.splits;
   p.set_heads = share.set_heads;
   p.head_sets = share.head_sets;
@@ -249,7 +250,6 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     const dim3 grid = per_request(static_cast<int64_t>(c.g.n_heads) * share.splits);
     e = c.fmt == kFP8 ? launch_prompt_fp8(p, grid, stream) : launch_prompt_int4(p, grid, stream);
   } else {
-    // the join of the waves needs more than 32 rows' second query parts
     size_t bytes = kRowsWaves * kWaveAreaBytes + (kRowsWaves / 2) * share.nt * (8192 + 512);
     if (share.ranges > 0) bytes += static_cast<size_t>(prefix_bytes(c.req));
     const dim3 grid = share.ranges > 0 ? dim3(static_cast<unsigned>(share.ranges * share.head_sets))

@@ -51,6 +51,7 @@ struct PromptShared {
   int32_t delta[4][kPromptTile];
   float top[kPromptWaves][2];          // largest and least row maximum of each wave
   float2 turn[QP > 1 ? kPromptWaves : 1][kHeadDim / 2];
+  h8 low[QP > 1 ? kPromptWaves : 1][8][kWave];     // second parts of the queries: registers are few
 };
 
 template <int FMT, int DT, int QP>
@@ -142,16 +143,19 @@ void attend_prompt_kernel(AttendParams p) {
     const float ks_scale = p.scale_log2 * __builtin_ldexpf(1.0f, e_all);
 
     // Queries as operands: dims 16 kk + 8 h + (0 .. 7) in the order of the codes.
-    h8 qf[QP][8];
+    h8 qf[8];
+    h8* low = &sh.low[QP > 1 ? wave : 0][0][lane];
     auto to_operand = [&](const float (&x)[8], int kk) __attribute__((always_inline)) {
+      h8 second;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
         const float v = __builtin_ldexpf(x[FMT == kINT4 ? kOrder[i] : i], -e_row);
         const _Float16 hi = static_cast<_Float16>(v);
-        qf[0][kk][i] = hi;
-        if constexpr (QP > 1) qf[1][kk][i] = static_cast<_Float16>(v - static_cast<float>(hi));
+        qf[kk][i] = hi;
+        if constexpr (QP > 1) second[i] = static_cast<_Float16>(v - static_cast<float>(hi));
       }
+      if constexpr (QP > 1) low[kk * kWave] = second;
     };
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
@@ -358,10 +362,11 @@ void attend_prompt_kernel(AttendParams p) {
               kf[kk] = *reinterpret_cast<const h8*>(sh.keys[t & 1] + (k_at ^ (kk << 5)));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-              for (int qp = QP - 1; qp >= 0; --qp)
-                a = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[kk], qf[qp][kk], a, 0, 0, 0);
+            for (int kk = 0; kk < 8; ++kk) {
+              if constexpr (QP > 1)
+                a = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[kk], low[kk * kWave], a, 0, 0, 0);
+              a = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[kk], qf[kk], a, 0, 0, 0);
+            }
           };
           if (QP > 1 && moves) {
             // one pass per distance among the 32 tokens

@@ -326,10 +326,7 @@ void attend_rows_kernel(AttendParams p) {
     // codes, times 2^-e.  The row's exponent puts its largest magnitude below
     // 2^14, so a turned one stays below 2^15; fp16 queries that do not turn
     // are operands as they are.
-    // (second parts of 32 rows: in LDS, they do not fit the registers)
-    constexpr bool kLowInLds = NT * QP == 4;
-    h8 qf[NT][kLowInLds ? 1 : QP][4];
-    h8* low = reinterpret_cast<h8*>(merge) + wave * NT * 4 * kWave + lane;
+    h8 qf[NT][QP][4];
     int e[NT];
     float grow[NT];                       // 2^e
     const int32_t* table = p.table + r * p.table_stride;
@@ -344,10 +341,7 @@ void attend_rows_kernel(AttendParams p) {
         qf[n][0][kk][j] = hi;
         if constexpr (QP > 1) second[j] = static_cast<_Float16>(v - static_cast<float>(hi));
       }
-      if constexpr (kLowInLds)
-        low[(n * 4 + kk) * kWave] = second;
-      else if constexpr (QP > 1)
-        qf[n][1][kk] = second;
+      if constexpr (QP > 1) qf[n][1][kk] = second;
     };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -558,9 +552,7 @@ void attend_rows_kernel(AttendParams p) {
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
               for (int qp = QP - 1; qp >= 0; --qp) {
-                const h8 q = kLowInLds && qp > 0 ? low[(n * 4 + kk) * kWave]
-                                                 : qf[n][kLowInLds ? 0 : qp][kk];
-                a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[kk], q, a, 0, 0, 0);
+                a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[kk], qf[n][qp][kk], a, 0, 0, 0);
               }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -884,16 +876,18 @@ template <int FMT, int DT>
 hipError_t launch_rows_dtype(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                              hipStream_t stream) {
   if (DT == kF32 || p.delta) {
-    if (hp == 2) return launch_rows_tiles<FMT, DT, 2, 1, 2>(p, grid, bytes, stream);
-    if (nt == 1) return launch_rows_tiles<FMT, DT, 1, 1, 2>(p, grid, bytes, stream);
+    // two parts per query: 32 rows of them leave the registers, and 16 rows
+    // twice over are faster (58 against 132 us for drafts of five tokens of 16
+    // requests over FP8 records)
+    return hp == 2 ? launch_rows_tiles<FMT, DT, 2, 1, 2>(p, grid, bytes, stream)
+                   : launch_rows_tiles<FMT, DT, 1, 1, 2>(p, grid, bytes, stream);
   }
   if constexpr (DT != kF32) {
-    if (p.delta) return launch_rows_tiles<FMT, DT, 1, 2, 2>(p, grid, bytes, stream);
     if (hp == 2) return launch_rows_tiles<FMT, DT, 2, 1, 1>(p, grid, bytes, stream);
     return nt == 1 ? launch_rows_tiles<FMT, DT, 1, 1, 1>(p, grid, bytes, stream)
                    : launch_rows_tiles<FMT, DT, 1, 2, 1>(p, grid, bytes, stream);
   }
-  return hipErrorInvalidValue;           // not reached: 32 rows of fp32 are never asked for
+  return hipErrorInvalidValue;           // not reached
 }
 
 template <int FMT>
