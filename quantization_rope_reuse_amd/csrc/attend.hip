@@ -2,9 +2,6 @@
 // and the join of partial results.
 #include "attend_rows.h"
 
-#ifndef HKV_PROMPT
-#define HKV_PROMPT 64
-#endif
 namespace hkv {
 namespace {
 
@@ -118,9 +115,15 @@ Share share_of(int fmt, bool moved, const Geometry& g, const hkv_requests& req, 
   const int64_t queries = req.max_queries < n_tokens ? req.max_queries : n_tokens;
   const int64_t rows = queries * (n_q_heads / g.n_heads);
   s.splits = 0;
-  if (rows > HKV_PROMPT) {
-    // one workgroup per 256 rows and key head; their tokens are cut where
-    // these are too few for the CUs
+  if (rows > 384) {
+    // The prompt kernel makes operands of codes once for 256 rows, the rows
+    // kernel for 32; but its eight waves wait for each other every 64 tokens.
+    // Of 32 query and 8 key heads behind 8,192 tokens, rows against prompt
+    // kernel: 40 queries of 2 requests 52 against 63 us, 100 queries 57
+    // against 57, 300 (behind 4,096) 71 against 66, 1,000 255 against 265
+    // (fp8) and with moved keys 409 against 387, fp32 641 against 540.
+    // One workgroup per 256 rows and key head; their tokens are cut where
+    // these are too few for the CUs.
     s.items = (rows + kPromptRows - 1) / kPromptRows;
     int64_t most = static_cast<int64_t>(n_tokens) * (n_q_heads / g.n_heads) / kPromptRows + req.n_requests;
     const int64_t all = req.n_requests * s.items;

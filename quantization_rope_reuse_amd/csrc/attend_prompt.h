@@ -464,8 +464,26 @@ void attend_prompt_kernel(AttendParams p) {
             big = fmaxf(big, fabsf(w[i]));
             little = fminf(little, fabsf(w[i]));
           }
-          if (__any(big > 61440.0f || sum > 0x1p110f)) {
-            // the reference moves
+          // Where a row's weights outgrow fp16, its reference moves: by a power of
+          // two while they are finite, found anew where they are not (or where
+          // the row does not see them all).
+          const bool anew = __any(!(big < INFINITY) || sum > 0x1p110f);
+          if (!anew && __any(big > 61440.0f)) {
+            const float most_w = fmaxf(big, __shfl_xor(big, 32));
+            const float up = most_w > 61440.0f ? rintf(__builtin_amdgcn_logf(most_w)) - 13.0f : 0.0f;
+            const float keep = __builtin_ldexpf(1.0f, -static_cast<int>(up));
+            m += up;
+            l *= keep;
+            sum *= keep;
+            little *= keep;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[d][i] *= keep;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] *= keep;
+          }
+          if (anew) {
             float want = kNoReference;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -473,10 +491,10 @@ void attend_prompt_kernel(AttendParams p) {
               const float lv = fminf(__builtin_amdgcn_logf(fabsf(vs[i])), 16.0f);
               const float x = fmaxf(s2 + lv, s2 - 80.0f);
               want = fmaxf(want, (vis >> i) & 1 ? x : kNoReference);
-              if ((i & 3) == 3) __builtin_amdgcn_sched_barrier(0);    // few registers at a time
+              if ((i & 7) == 7) __builtin_amdgcn_sched_barrier(0);    // few registers at a time
             }
             want = fmaxf(want, __shfl_xor(want, 32));
-            const float m_new = fmaxf(m, rintf(want));
+            const float m_new = fmaxf(m, rintf(want) + 1.0f);
             const float keep = m == m_new ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
             m = m_new;
             l *= keep;

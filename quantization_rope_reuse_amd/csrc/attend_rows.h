@@ -21,9 +21,10 @@
 //
 // Softmax: weights w = 2^14 exp2(s - m) v_scale enter their product as fp16, so
 // m is a reference (a whole number) that keeps both w (fp16) and the sum's
-// terms (fp32) finite.  It moves only when a tile would leave that range, to
-// the tile's largest s + log2(v_scale) or largest s - 80: seldom after the
-// first tile, which spares the rescaling of O and the reductions across lanes.
+// terms (fp32) finite.  It moves only when a tile would leave that range, to a
+// little above the tile's largest s + log2(v_scale) or the largest s - 80:
+// seldom after the first tile, which spares the rescaling of O and the
+// reductions across lanes.
 // Near the largest weight s - m is small, so its rounding is.  Weights below
 // fp16's normal numbers, 2^-28 of the largest (2^-17 where two parts are to
 // hold 22 bits), would lose their last bits, which shows where all heavier
@@ -657,7 +658,8 @@ void attend_rows_kernel(AttendParams p) {
         if constexpr (PP > 1) pf[n][1][i] = static_cast<_Float16>(y - static_cast<float>(hi));
       };
       float sv[NT][8], w[NT][8], sum[NT];
-      bool leave = false;
+      float big[NT];
+      bool leave = false, anew = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -666,17 +668,45 @@ void attend_rows_kernel(AttendParams p) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const bool vis = ((mine >> i) & 1) && static_cast<uint32_t>(t * kTileTokens + 8 * g + i) <
-                                                                     static_cast<uint32_t>(sees[n]);
+                                                      static_cast<uint32_t>(sees[n]);
             sv[n][i] = vis ? sv[n][i] : -INFINITY;
           }
         }
         weights(w[n], sv[n], n, &sum[n]);
-        float top = fabsf(w[n][0]);
+        // a token that the row does not see weighs nothing whatever its scale
+        if (part) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, fabsf(w[n][i]));
-        leave = leave || top > 61440.0f || sum[n] > 0x1p96f;
+          for (int i = 0; i < 8; ++i) w[n][i] = sv[n][i] == -INFINITY ? 0.0f : w[n][i];
+        }
+        big[n] = fabsf(w[n][0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) big[n] = fmaxf(big[n], fabsf(w[n][i]));
+        leave = leave || big[n] > 61440.0f;
+        anew = anew || !(big[n] < INFINITY) || sum[n] > 0x1p96f;
       }
-      if (__any(leave)) {
+      // Where a row's weights outgrow fp16, its reference moves: by a power of
+      // two while they are finite, found anew where they are not.
+      // (Of 32 rows always anew: both ways would cost the usual one registers.)
+      anew = __any(NT == 1 ? anew : anew || leave);
+      if (NT == 1 && !anew && __any(leave)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float most = fmaxf(big[n], __shfl_xor(big[n], 16));
+          most = fmaxf(most, __shfl_xor(most, 32));
+          const float up = most > 61440.0f ? rintf(__builtin_amdgcn_logf(most)) - 13.0f : 0.0f;
+          const float keep = __builtin_ldexpf(1.0f, -static_cast<int>(up));
+          st.m[n] += up;
+          st.l[n] *= keep;
+          sum[n] *= keep;
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.o[n][d][i] *= keep;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[n][i] *= keep;
+        }
+      }
+      if (anew) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float want = kNoReference;
@@ -688,7 +718,7 @@ void attend_rows_kernel(AttendParams p) {
           }
           want = fmaxf(want, __shfl_xor(want, 16));
           want = fmaxf(want, __shfl_xor(want, 32));
-          const float m = fmaxf(st.m[n], rintf(want));
+          const float m = fmaxf(st.m[n], rintf(want) + 1.0f);
           const float keep = st.m[n] == m ? 1.0f : __builtin_amdgcn_exp2f(st.m[n] - m);
           st.m[n] = m;
           st.l[n] *= keep;
@@ -697,6 +727,10 @@ void attend_rows_kernel(AttendParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) st.o[n][d][i] *= keep;
           weights(w[n], sv[n], n, &sum[n]);
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[n][i] = sv[n][i] == -INFINITY ? 0.0f : w[n][i];
+          }
         }
       }
       constexpr float kSmall = PP > 1 ? 0x1p-3f : 0x1p-14f;
@@ -704,11 +738,6 @@ void attend_rows_kernel(AttendParams p) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         st.l[n] += sum[n];
-        // a token that the row does not see weighs nothing whatever its scale
-        if (part) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[n][i] = sv[n][i] == -INFINITY ? 0.0f : w[n][i];
-        }
         float least = fabsf(w[n][0]);
 #pragma unroll
         for (int i = 1; i < 8; ++i) least = fminf(least, fabsf(w[n][i]));
