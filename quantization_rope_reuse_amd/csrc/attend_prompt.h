@@ -61,8 +61,8 @@ void attend_prompt_kernel(AttendParams p) {
   constexpr int CB = FMT == kFP8 ? kHeadDim : kHeadDim / 2;
   constexpr int W = CB / 64;
   constexpr int ES = ElemSize<DT>::value;
-  constexpr int PP = DT == kF32 ? 2 : 1;
-  constexpr float kSmall = PP > 1 ? 0x1p-3f : 0x1p-14f;
+  constexpr int PP = DT == kBF16 ? 1 : 2;
+  constexpr float kSmall = DT == kF32 ? 0x1p-3f : 0x1p-14f;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   PromptShared<DT, QP>& sh = *reinterpret_cast<PromptShared<DT, QP>*>(lds);
   const int tid = threadIdx.x;

@@ -191,7 +191,7 @@ void attend_rows_kernel(AttendParams p) {
   constexpr int CB = FMT == kFP8 ? kHeadDim : kHeadDim / 2;
   constexpr int W = CB / 64;                  // dwords per 8 codes
   constexpr int ES = ElemSize<DT>::value;
-  constexpr int PP = DT == kF32 ? 2 : 1;
+  constexpr int PP = DT == kBF16 ? 1 : 2;
   static_assert(HP == 1 || NT == 1, "two heads share one score tile");
   constexpr int kItemRows = 16 * NT / HP;
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -222,60 +222,76 @@ void attend_rows_kernel(AttendParams p) {
   // The work: this workgroup's range of the tiles of all items, or (one
   // request per blockIdx.y) whole items.
   uint32_t at = 0, end = 0;            // flat tiles
-  int r, item = range, items = 0;
+  int r = 0, item = range, items = 0;
+  const int R = p.n_requests;
+  const bool few = R <= kWave;         // a wave's lanes hold the requests' tiles
+  uint32_t run = 0;                    // tiles up to and with this lane's request
+  auto tiles_of_request = [&](int q) {
+    const Span s = span_of(p, q);
+    return static_cast<uint32_t>((s.rows + kItemRows - 1) / kItemRows) * tiles_of(s);
+  };
   if (p.ranges > 0) {
-    const int R = p.n_requests;
-    constexpr int kPer = kMaxFlatRequests / kRowsThreads;
-    uint32_t own[kPer], sum = 0;
+    uint32_t total;
+    if (few) {
+      // every wave for itself, without LDS or a barrier
+      run = lane < R ? tiles_of_request(lane) : 0;
+      if (R > 1) {
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int q = threadIdx.x * kPer + u;
-      own[u] = 0;
-      if (q < R) {
-        const Span s = span_of(p, q);
-        own[u] = static_cast<uint32_t>((s.rows + kItemRows - 1) / kItemRows) * tiles_of(s);
+        for (int off = 1; off < kWave; off <<= 1) {
+          const uint32_t o = __shfl_up(run, off);
+          if (lane >= off) run += o;
+        }
       }
-      sum += own[u];
-    }
-    uint32_t run = sum;
-    if (R > 1) {
+      total = __builtin_amdgcn_readlane(run, R - 1);
+      if (lane >= R) run = total;
+    } else {
+      const int per_thread = (R + kRowsThreads - 1) / kRowsThreads;
+      const int q0 = min(static_cast<int>(threadIdx.x) * per_thread, R);
+      const int q1 = min(q0 + per_thread, R);
+      uint32_t sum = 0;
+      for (int q = q0; q < q1; ++q) sum += tiles_of_request(q);
+      uint32_t upto = sum;
 #pragma unroll
       for (int off = 1; off < kWave; off <<= 1) {
-        const uint32_t o = __shfl_up(run, off);
-        if (lane >= off) run += o;
+        const uint32_t o = __shfl_up(upto, off);
+        if (lane >= off) upto += o;
       }
+      uint32_t* wave_sum = reinterpret_cast<uint32_t*>(merge);
+      if (lane == kWave - 1) wave_sum[wave] = upto;
+      __syncthreads();
+      uint32_t before = upto - sum;
+      for (int w = 0; w < wave; ++w) before += wave_sum[w];
+      for (int q = q0; q < q1; ++q) {
+        prefix[q] = before;
+        before += tiles_of_request(q);
+      }
+      if (threadIdx.x == kRowsThreads - 1) prefix[R] = before;   // its q1 is R
+      __syncthreads();
+      total = prefix[R];
     }
-    uint32_t* wave_sum = reinterpret_cast<uint32_t*>(merge);
-    if (lane == kWave - 1) wave_sum[wave] = run;
-    __syncthreads();
-    uint32_t before = run - sum;
-    for (int w = 0; w < wave; ++w) before += wave_sum[w];
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int q = threadIdx.x * kPer + u;
-      if (q <= R) prefix[q] = before;
-      before += own[u];
-    }
-    if (R == kMaxFlatRequests && threadIdx.x == kRowsThreads - 1) prefix[R] = before;
-    __syncthreads();
-    const uint32_t total = prefix[R];
     const uint32_t per = max((total + p.ranges - 1) / p.ranges, static_cast<uint32_t>(p.min_tiles));
     at = min(range * per, total);       // range * per < total + per * ranges: below 2^32
     end = min(at + per, total);
     if (p.prefix_out && blockIdx.x == 0) {
-      for (int q = threadIdx.x; q <= R; q += kRowsThreads) p.prefix_out[q] = prefix[q];
+      if (few) {
+        if (wave == 0 && lane < R) p.prefix_out[lane + 1] = run;
+        if (threadIdx.x == 0) p.prefix_out[0] = 0;
+      } else {
+        for (int q = threadIdx.x; q <= R; q += kRowsThreads) p.prefix_out[q] = prefix[q];
+      }
       if (threadIdx.x == 0) p.prefix_out[R + 1] = per;
     }
     if (at >= end) return;
-    int lo = 0, hi = R;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= at)
-        lo = mid;
-      else
-        hi = mid;
+    if (!few) {
+      int hi = R;
+      while (hi - r > 1) {
+        const int mid = (r + hi) >> 1;
+        if (prefix[mid] <= at)
+          r = mid;
+        else
+          hi = mid;
+      }
     }
-    r = lo;
   } else {
     r = blockIdx.y;
     items = (span_of(p, r).rows + kItemRows - 1) / kItemRows;
@@ -286,14 +302,22 @@ void attend_rows_kernel(AttendParams p) {
   while (p.ranges > 0 ? at < end : item < items) {
     if (again) __syncthreads();          // the merge area is free again
     again = true;
-    if (p.ranges > 0)
-      while (prefix[r + 1] <= at) ++r;   // requests without items
+    uint32_t first = 0;                  // tiles before request r
+    if (p.ranges > 0) {
+      if (few) {
+        r = __popcll(__ballot(run <= at));
+        first = r > 0 ? __builtin_amdgcn_readlane(run, r - 1) : 0;
+      } else {
+        while (prefix[r + 1] <= at) ++r; // requests without items
+        first = prefix[r];
+      }
+    }
     const Span s = span_of(p, r);
     const int tiles = tiles_of(s);
     int t0 = 0;
     if (p.ranges > 0) {
-      item = (at - prefix[r]) / static_cast<uint32_t>(tiles);
-      t0 = at - prefix[r] - item * tiles;
+      item = (at - first) / static_cast<uint32_t>(tiles);
+      t0 = at - first - item * tiles;
     }
     int t1 = tiles;
     if (p.ranges > 0 && end - at < static_cast<uint32_t>(tiles - t0))
@@ -301,7 +325,8 @@ void attend_rows_kernel(AttendParams p) {
     const bool whole = t0 == 0 && t1 == tiles;
     const int row0 = item * kItemRows;
 
-    // Rows of this lane, and what they see.
+    // Rows of this lane, and what they see.  (A division is some 30 instructions.)
+    const bool one_query = s.rows <= p.group;
     const char* q_row[NT];
     int sees[NT], query[NT], head[NT];
     bool real[NT];
@@ -311,14 +336,14 @@ void attend_rows_kernel(AttendParams p) {
       const int row = row0 + 16 * n + (HP == 2 ? c & 7 : c);
       real[n] = row < s.rows;
       const int clamped = min(row, s.rows - 1);
-      const int j = clamped / p.group;
+      const int j = one_query ? 0 : clamped / p.group;
       query[n] = s.start + j;
       head[n] = (HP == 2 ? kh0 + (c >> 3) : kh0) * p.group + (clamped - j * p.group);
       q_row[n] = p.q + query[n] * p.q_token + head[n] * p.q_head;
       sees[n] = max(p.causal ? s.len - s.n_q + j + 1 : s.len, 0);
     }
-    const int j_first = row0 / p.group;
-    const int j_last = (min(row0 + kItemRows, s.rows) - 1) / p.group;
+    const int j_first = one_query ? 0 : row0 / p.group;
+    const int j_last = one_query ? 0 : (min(row0 + kItemRows, s.rows) - 1) / p.group;
     const int sees_least = p.causal ? s.len - s.n_q + j_first + 1 : s.len;
     const int sees_most = p.causal ? s.len - s.n_q + j_last + 1 : s.len;
     last = min(t1, max(sees_most, 0) / kTileTokens + (max(sees_most, 0) % kTileTokens != 0));
@@ -733,7 +758,7 @@ void attend_rows_kernel(AttendParams p) {
           }
         }
       }
-      constexpr float kSmall = PP > 1 ? 0x1p-3f : 0x1p-14f;
+      constexpr float kSmall = DT == kF32 ? 0x1p-3f : 0x1p-14f;
       bool small = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
