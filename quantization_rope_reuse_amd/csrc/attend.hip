@@ -136,23 +136,33 @@ Share share_of(int fmt, bool moved, const Geometry& g, const hkv_requests& req, 
     s.rows = s.splits > 1 ? static_cast<int64_t>(s.splits) * n_tokens * n_q_heads : 0;
     return s;
   }
-  // Two heads of at most 8 rows share a score tile, which halves the softmax
-  // and the bookkeeping of each.
-  s.hp = rows <= 8 && g.n_heads % 2 == 0 ? 2 : 1;
   s.nt = dtype == kF32 || moved || rows <= 16 ? 1 : 2;
-  const int64_t item_rows = 16 * s.nt / s.hp;
-  s.items = (rows + item_rows - 1) / item_rows;
   const int64_t max_len = static_cast<int64_t>(req.max_blocks) * g.block_tokens;
   const int64_t tiles = max_len < kTileTokens ? 1 : (max_len + kTileTokens - 1) / kTileTokens;
-  // Two INT4 heads of a token share a 128-byte line, so one workgroup reads both.
-  s.set_heads = s.hp == 1 && fmt == kINT4 && g.n_heads % 2 == 0 ? 2 : 1;
+  // Two heads of at most 8 rows share a score tile, which halves the softmax
+  // and the bookkeeping of each; and two INT4 heads of a token share a
+  // 128-byte line, so one workgroup reads both.  Short work goes faster with
+  // a workgroup for every head (one request of 777 tokens 11.6 against 12.4
+  // us, of 3,000 12.6 against 12.9, of 8,000 16.9 against 15.1; 16 requests of
+  // up to 1,000 16.4 against 20.5; 32 query and 8 key heads).
+  const int64_t work = static_cast<int64_t>(req.n_requests) * g.n_heads * tiles;
+  const bool paired = g.n_heads % 2 == 0 && (tiles > 32 ? work > 1024 : work > 8192);
+  s.hp = paired && rows <= 8 ? 2 : 1;
+  const int64_t item_rows = 16 * s.nt / s.hp;
+  s.items = (rows + item_rows - 1) / item_rows;
+  s.set_heads = s.hp == 1 && paired && fmt == kINT4 ? 2 : 1;
   s.head_sets = g.n_heads / (s.set_heads * s.hp);
   const int64_t phases = kRowsWaves / s.set_heads;
   s.ranges = 0;
   s.min_tiles = static_cast<int>(phases);
   s.part_rows = static_cast<int>(rows < item_rows ? rows : item_rows);
   const int64_t all = static_cast<int64_t>(req.n_requests) * s.items * tiles;
-  if (req.n_requests <= kMaxFlatRequests && tiles > 4 * phases && queries * n_q_heads <= (1 << 20) &&
+  // Requests of few tiles keep them to one workgroup per head and spare the
+  // join (16 requests of up to 1,000 tokens: 16.4 against 22.2 us), unless
+  // there are too few of them to keep more than a few CUs at work (one request
+  // of 777: 14.0 against 11.6).
+  const int64_t few = static_cast<int64_t>(req.n_requests) * g.n_heads >= 32 ? 32 : 16;
+  if (req.n_requests <= kMaxFlatRequests && tiles > few && queries * n_q_heads <= (1 << 20) &&
       all < (int64_t{1} << 30)) {
     int64_t ranges = 512 / s.head_sets;
     const int64_t most = (all + s.min_tiles - 1) / s.min_tiles;
