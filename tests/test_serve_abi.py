@@ -236,3 +236,9 @@ def test_binding_requires_gpu_tensors():
         H.append_tokens(x, x, i.long(), rec, "fp8", 16)
     with pytest.raises(ValueError, match="on a GPU"):
         H.attend_records(x, rec, "fp8", 16, 8, torch.zeros(4, 8, dtype=torch.int32), i)
+
+
+def test_attend_many_heads_unsupported():
+    many = 4097
+    shape, rec = _shape(n_kv_heads=many, block_tokens=1), _recs(block_stride_bytes=1 << 21)
+    assert _attend(shape=shape, rec=rec, q=_h(many, many * 128), out=_h(many, many * 128)) == H.ERR_UNSUPPORTED
