@@ -42,31 +42,33 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendParams p) {
   constexpr int ES = ElemSize<SDT>::value;
   const int lane = threadIdx.x & (kWave - 1);
   const int sub = lane & (kLanesPerVec - 1);
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * (kThreads / kWave) + threadIdx.x / kWave;
-  const int64_t v = wave * kVecsPerWave + lane / kLanesPerVec;
-  if (wave * kVecsPerWave >= p.n_vecs) return;            // whole wave
-  const int64_t vc = v < p.n_vecs ? v : p.n_vecs - 1;     // lanes past the end repeat the last
-  const int kv = blockIdx.y;
-  const int64_t t = divide(vc, p.n_heads, p.rcp_heads);
-  const int h = static_cast<int>(vc - t * p.n_heads);
-  const int64_t slot = p.slots[t];
-  const bool active = v < p.n_vecs && slot >= 0 && slot < p.n_slots;
-  const char* src = (kv ? p.v + t * p.v_token + h * p.v_head : p.k + t * p.k_token + h * p.k_head) +
-                    8 * sub * ES;
-  const RawSrc<SDT> ra = load_run<SDT>(src);
-  const RawSrc<SDT> rb = load_run<SDT>(src + 64 * ES);
-  const int64_t s = active ? slot : 0;
-  const int64_t blk = divide(s, p.block_tokens, p.rcp_block);
-  const int at = static_cast<int>(s - blk * p.block_tokens) * p.n_heads + h;
-  uint8_t* rec = p.rec + blk * p.rec_block;
-  float a[8], b[8];
-  run_to_f32<SDT>(ra, a);
-  run_to_f32<SDT>(rb, b);
-  const uint32_t sbits = quant_vector<FMT, false>(
-      a, b, rec + (static_cast<int64_t>(kv) * p.vecs + at) * CB, sub, active, nullptr);
-  if (active && sub == 0)
-    reinterpret_cast<uint16_t*>(rec + 2LL * p.vecs * CB)[static_cast<int64_t>(kv) * p.vecs + at] =
-        static_cast<uint16_t>(sbits);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / kWave);
+  for (int64_t wave = static_cast<int64_t>(blockIdx.x) * (kThreads / kWave) + threadIdx.x / kWave;
+       wave * kVecsPerWave < p.n_vecs; wave += step) {
+    const int64_t v = wave * kVecsPerWave + lane / kLanesPerVec;
+    const int64_t vc = v < p.n_vecs ? v : p.n_vecs - 1;     // lanes past the end repeat the last
+    const int kv = blockIdx.y;
+    const int64_t t = divide(vc, p.n_heads, p.rcp_heads);
+    const int h = static_cast<int>(vc - t * p.n_heads);
+    const int64_t slot = p.slots[t];
+    const bool active = v < p.n_vecs && slot >= 0 && slot < p.n_slots;
+    const char* src = (kv ? p.v + t * p.v_token + h * p.v_head : p.k + t * p.k_token + h * p.k_head) +
+                      8 * sub * ES;
+    const RawSrc<SDT> ra = load_run<SDT>(src);
+    const RawSrc<SDT> rb = load_run<SDT>(src + 64 * ES);
+    const int64_t s = active ? slot : 0;
+    const int64_t blk = divide(s, p.block_tokens, p.rcp_block);
+    const int at = static_cast<int>(s - blk * p.block_tokens) * p.n_heads + h;
+    uint8_t* rec = p.rec + blk * p.rec_block;
+    float a[8], b[8];
+    run_to_f32<SDT>(ra, a);
+    run_to_f32<SDT>(rb, b);
+    const uint32_t sbits = quant_vector<FMT, false>(
+        a, b, rec + (static_cast<int64_t>(kv) * p.vecs + at) * CB, sub, active, nullptr);
+    if (active && sub == 0)
+      reinterpret_cast<uint16_t*>(rec + 2LL * p.vecs * CB)[static_cast<int64_t>(kv) * p.vecs + at] =
+          static_cast<uint16_t>(sbits);
+  }
 }
 
 template <int FMT>
@@ -107,7 +109,9 @@ hipError_t launch_append(int fmt, int dtype, const Geometry& g, const HeadView& 
   p.vecs = g.vecs;
   p.n_vecs = static_cast<int64_t>(n_tokens) * g.n_heads;
   constexpr int64_t per_wg = kVecsPerWave * (kThreads / kWave);
-  const dim3 grid(static_cast<unsigned>((p.n_vecs + per_wg - 1) / per_wg), 2);
+  // a launch holds less than 2^32 threads: vectors beyond 2^22 workgroups go round
+  const int64_t need = (p.n_vecs + per_wg - 1) / per_wg;
+  const dim3 grid(static_cast<unsigned>(need < (1 << 22) ? need : 1 << 22), 2);
   return fmt == kFP8 ? launch_fmt<kFP8>(dtype, p, grid, stream)
                      : launch_fmt<kINT4>(dtype, p, grid, stream);
 }
