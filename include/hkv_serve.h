@@ -171,6 +171,12 @@ typedef struct {
  * a row that sees nothing gets out = 0 and lse = -infinity.  k_m and v_m are
  * code * scale, taken into the products exactly: codes enter the matrix
  * instructions as they are and scales multiply scores and weights in fp32.
+ * Sums are fp32.  Queries enter as fp16 where that is exact, else (fp32, or
+ * turned by a shift) as two fp16 parts, 22 bits; weights as one fp16 part for
+ * bf16 results, as two for the others.
+ * What a token holds does not matter where its table entry is out of range or
+ * where it stands past the end; a token that a row merely may not see yet must
+ * not hold a NaN code (hkv_quant_* and hkv_append_tokens never write one).
  * q and out: dtype, n_tokens rows, the same number of heads, a multiple of
  * n_kv_heads; out must not overlap q.  lse: float [n_tokens][n_heads], or
  * NULL.  Rows of no request keep what out and lse held.

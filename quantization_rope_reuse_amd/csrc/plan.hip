@@ -12,7 +12,8 @@
 // than waiting for a launch of its own to publish them: with at most 4,096
 // requests that is at most 8 per thread and 32 KB read from L2.  The
 // tokens, the pushed and the popped blocks are then spread over all threads
-// of the grid, each finding its request by binary search in LDS.
+// of the grid, each finding its request by binary search in LDS.  48 decoding
+// requests take 6 us, 1,500 requests with 40 prompts (62,000 tokens) 9.
 #include "hkv_device.h"
 #include "serve_launch.h"
 
