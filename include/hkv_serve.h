@@ -118,7 +118,8 @@ typedef struct {
  * must not overlap them otherwise.  positions: int32, entry (axis a, token t)
  * at positions + a*axis_stride + t.  inverse != 0 turns by -phi: the
  * gradient of this call with respect to q and k, given that of its outputs
- * (a rotation's transpose), and the way to strip positions. */
+ * (a rotation's transpose), and the way to strip positions.  More than 2^24
+ * heads in all, or n_tokens times them above 2^31 - 1: HKV_ERR_UNSUPPORTED. */
 int hkv_rope_heads(const hkv_rope_axes* rope, const int32_t* positions, int64_t axis_stride,
                    int32_t n_tokens, const hkv_heads* q, const hkv_heads* k,
                    const hkv_heads* q_out, const hkv_heads* k_out, int32_t dtype,
@@ -129,7 +130,8 @@ int hkv_rope_heads(const hkv_rope_axes* rope, const int32_t* positions, int64_t 
  * (int64, device), bit for bit what hkv_quant_fp8 / hkv_quant_int4 write for
  * the same vectors.  Slots outside [0, n_blocks * block_tokens) are skipped;
  * no two tokens may share a slot.  Other tokens of a block, their codes and
- * scales, are not touched. */
+ * scales, are not touched.  n_tokens * n_kv_heads above 2^31 - 1:
+ * HKV_ERR_UNSUPPORTED. */
 int hkv_append_tokens(const hkv_shape* shape, int32_t fmt, const hkv_heads* k, const hkv_heads* v,
                       int32_t dtype, int32_t n_tokens, const int64_t* slots,
                       const hkv_records* dst, hipStream_t stream);
@@ -176,7 +178,8 @@ typedef struct {
  * bf16 results, as two for the others.
  * What a token holds does not matter where its table entry is out of range or
  * where it stands past the end; a token that a row merely may not see yet must
- * not hold a NaN code (hkv_quant_* and hkv_append_tokens never write one).
+ * not hold a NaN code (hkv_quant_* and hkv_append_tokens write none for
+ * finite values).
  * q and out: dtype, n_tokens rows, the same number of heads, a multiple of
  * n_kv_heads; out must not overlap q.  lse: float [n_tokens][n_heads], or
  * NULL.  Rows of no request keep what out and lse held.

@@ -291,7 +291,17 @@ py::tuple attend_records(const Tensor& q, const Tensor& records, int fmt, int64_
   const int dtype = dtype_of(q);
   if (make) {
     const int64_t bytes = calls.attend_bytes(&pool.shape, &req, small(n, "n_tokens"), qh.n_heads, dtype);
-    if (bytes > 0) ws = at::empty({bytes}, q.options().dtype(at::kByte));
+    if (bytes > 0) {
+      ws = at::empty({bytes}, q.options().dtype(at::kByte));
+      // the allocator hands it out again only when the call's stream is done
+      if (!stream.is_none()) {
+        const py::object on_stream =
+            PyLong_Check(stream.ptr())
+                ? py::module_::import("torch").attr("cuda").attr("ExternalStream")(stream, py::cast(on.device()))
+                : stream;
+        py::cast(*ws).attr("record_stream")(on_stream);
+      }
+    }
   }
   if (ws) need(ws->scalar_type() == at::kByte && ws->is_contiguous(), "workspace must be a contiguous uint8 tensor");
   const hkv_heads oh = heads_of(out, "out");

@@ -147,6 +147,28 @@ def test_same_call_same_bits():
         assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_on_another_stream(handle):
+    """A call on another stream than the current one, its workspace made by the
+    call, while the current stream takes and fills memory of that size."""
+    fmt, dtype, tb, h, group, lens, asks = "int4", "bf16", 64, 2, 8, [9000], [1]
+    _, rec, table, q_start, q = setup(4, fmt, dtype, tb, h, group, lens, asks)
+    t, n = dev(table), dev(np.asarray(lens, np.int32))
+    want, _ = hkv.attend_records(q, rec, fmt, tb, h, t, n)
+    need = hkv.attend_workspace_bytes(rec.shape[0], tb, h, 1, table.shape[1], 1, h * group, 1, q.dtype)
+    assert need > 0
+    side = torch.cuda.Stream()
+    outs = [torch.empty_like(q) for _ in range(20)]
+    lse = torch.empty(q.shape[:2], device=DEV)
+    torch.cuda.synchronize()
+    for out in outs:
+        hkv.attend_records(q, rec, fmt, tb, h, t, n, out=out, lse=lse, stream=side.cuda_stream if handle else side)
+        torch.empty(need, dtype=torch.uint8, device=DEV).fill_(0xFF)
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out, want)
+
+
 def test_python_refusals():
     """Types, shapes and strides that the C calls cannot see."""
     i = torch.zeros(4, dtype=torch.int32, device=DEV)
