@@ -228,13 +228,18 @@ void attend_prompt_kernel(AttendParams p) {
     // the others more often than their products.
     auto bring = [&](int t) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
+      const int id = here(tid);
+      const int k_token = k_token_of(id), k_part = id & 7, v_col = id & 15, v_token = v_token_of(id);
+      // (tile t + 2's offsets: read first, they arrive behind the conversions)
+      const int64_t k_off = sh.vec[t & 1][k_token];
+      const int64_t v_offs[2] = {sh.vec[t & 1][v_token], sh.vec[t & 1][v_token + 1]};
+      const int64_t s_off = sh.scale[t & 1][lane];
+      const uint64_t live = sh.live[(t + 1) & 3];
+      __builtin_amdgcn_sched_barrier(0);
       // Tile t + 1: codes to operands.
       if (t + 1 >= t0 && t + 1 < t1) {
         const int b = (t + 1) & 1;
         char* values = sh.values[b];
-        const uint64_t live = sh.live[(t + 1) & 3];
-        const int id = here(tid);
-        const int k_token = k_token_of(id), k_part = id & 7, v_col = id & 15, v_token = v_token_of(id);
         char* krow = sh.keys[b] + k_token * 256;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -295,10 +300,7 @@ void attend_prompt_kernel(AttendParams p) {
       __builtin_amdgcn_sched_barrier(0);
       // Tile t + 2: its codes and scales set out.
       if (t + 2 >= t0 && t + 2 < t1) {
-        const int b = (t + 2) & 1;
-        const int id = here(tid);
-        const int k_token = k_token_of(id), k_part = id & 7, v_col = id & 15, v_token = v_token_of(id);
-        const uint8_t* ksrc = p.rec + sh.vec[b][k_token] + 2 * W * 4 * k_part;
+        const uint8_t* ksrc = p.rec + k_off + 2 * W * 4 * k_part;
         if constexpr (FMT == kINT4) {
           const u32x2 x = *reinterpret_cast<const u32x2*>(ksrc);
           raw_k[0] = x[0];
@@ -308,7 +310,7 @@ void attend_prompt_kernel(AttendParams p) {
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint8_t* vsrc = p.rec + sh.vec[b][v_token + i] + v_off + 4 * W * v_col;
+          const uint8_t* vsrc = p.rec + v_offs[i] + v_off + 4 * W * v_col;
           if constexpr (W == 1) {
             raw_v[i][0] = *reinterpret_cast<const uint32_t*>(vsrc);
           } else {
@@ -318,7 +320,7 @@ void attend_prompt_kernel(AttendParams p) {
           }
         }
         if (wave < 2)
-          raw_s = *reinterpret_cast<const uint16_t*>(p.rec + sh.scale[b][lane] +
+          raw_s = *reinterpret_cast<const uint16_t*>(p.rec + s_off +
                                                      (wave == 0 ? 0 : 2 * static_cast<int64_t>(p.vecs)));
       }
       // Tiles t + 3 and t + 4: the tokens' offsets, and their table entries.
