@@ -119,9 +119,9 @@ Share share_of(int fmt, bool moved, const Geometry& g, const hkv_requests& req, 
     // The prompt kernel makes operands of codes once for 256 rows, the rows
     // kernel for 32; but its eight waves wait for each other every 64 tokens.
     // Of 32 query and 8 key heads behind 8,192 tokens, rows against prompt
-    // kernel: 40 queries of 2 requests 52 against 63 us, 100 queries 57
-    // against 57, 300 (behind 4,096) 71 against 66, 1,000 255 against 265
-    // (fp8) and with moved keys 409 against 387, fp32 641 against 540.
+    // kernel: 40 queries of 2 requests 52 against 63 us, 100 queries 56
+    // against 56, 300 (behind 4,096) 69 against 66, 1,000 over FP8 258 against
+    // 260, with moved keys 434 against 364, fp32 663 against 530.
     // One workgroup per 256 rows and key head; their tokens are cut where
     // these are too few for the CUs.
     s.items = (rows + kPromptRows - 1) / kPromptRows;

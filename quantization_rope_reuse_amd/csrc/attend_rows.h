@@ -683,7 +683,8 @@ void attend_rows_kernel(AttendParams p) {
         }
       }
       h8 pf[NT][PP];
-      auto weights = [&](float (&w)[8], const float (&sv)[8], int n, float* sum) __attribute__((always_inline)) {
+      auto weights = [&](float (&w)[8], const float (&sv)[8], int n,
+                         float* sum) __attribute__((always_inline)) {
         float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
