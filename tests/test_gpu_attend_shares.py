@@ -202,3 +202,55 @@ def test_python_refusals():
         hkv.attend_records(x, rec, "fp8", 16, 8, t, i, max_queries=0)
     with pytest.raises(hkv.HkvError):
         hkv.attend_records(x[:, :7].contiguous(), rec, "fp8", 16, 8, t, i)
+
+
+@pytest.mark.parametrize("case", [("int4", "bf16", 64, 2, 8, [3000], [1]), PROMPTS[0], PROMPTS[4]],
+                         ids=["ranges", "prompt", "cut prompt"])
+def test_in_a_graph(case):
+    """Captured with a caller's workspace and replayed, with other lengths and
+    eager work between the replays; each replay has the eager call's bits."""
+    fmt, dtype, tb, h, group, lens, asks = case
+    _, rec, table, q_start, q = setup(6, fmt, dtype, tb, h, group, lens, asks)
+    t, n, qs = dev(table), dev(np.asarray(lens, np.int32)), dev(q_start.astype(np.int32))
+    need = hkv.attend_workspace_bytes(rec.shape[0], tb, h, len(lens), table.shape[1], sum(asks), h * group, max(asks),
+                                      q.dtype)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+
+    def call(o, s):
+        hkv.attend_records(q, rec, fmt, tb, h, t, n, q_start=qs, max_queries=max(asks), out=o, lse=s, workspace=ws)
+    call(out, lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, lse)
+    for cut in (0, 1, 60, 0):
+        n.copy_(dev(np.asarray(lens, np.int32) - cut))
+        want, want_lse = torch.empty_like(q), torch.empty_like(lse)
+        call(want, want_lse)
+        torch.cuda.synchronize()
+        out.fill_(7)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_rope_gradient_against_differences():
+    """<w, rope(x + e) - rope(x)> = <inverse(w), e> in fp32.  Each of the four
+    results is off by 2^-22 + 3 * 2^-24 of the pair it turns (angles in double),
+    each product by what it multiplies; x, e and w below 8."""
+    g = torch.Generator(DEV).manual_seed(12)
+    n, heads = 37, 3
+    x, e, w = (torch.randn(n, heads, 128, device=DEV, generator=g) for _ in range(3))
+    pos = torch.randint(0, 100000, (3, n), dtype=torch.int32, device=DEV, generator=g)
+    kw = dict(sections=(24, 20, 20), order="interleaved")
+    for pairs in ("interleaved", "half_split"):
+        a, _ = hkv.rope_heads(x + e, None, pos, 5e5, pairs, **kw)
+        b, _ = hkv.rope_heads(x, None, pos, 5e5, pairs, **kw)
+        back, _ = hkv.rope_heads(w, None, pos, 5e5, pairs, inverse=True, **kw)
+        step = ((x + e).double() - x.double())
+        left, right = (w.double() * (a.double() - b.double())), (back.double() * step)
+        bound = (2.0 ** -22 + 3 * 2.0 ** -24) * 4 * 16 * 8     # a pair's |a| + |b| <= 16, times 8
+        assert abs(float((left - right).sum())) <= bound * (n * heads * 128) ** 0.5 + bound
+        assert float((left.sum((1, 2)) - right.sum((1, 2))).abs().max()) <= bound * (heads * 128) ** 0.5 + bound
