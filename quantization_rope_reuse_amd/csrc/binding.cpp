@@ -74,10 +74,26 @@ class OneGpu {
   std::optional<at::Device> device_;
 };
 
-hipStream_t stream_of(const py::object& stream, at::Device device) {
-  if (stream.is_none()) return c10::hip::getCurrentHIPStream(device.index()).stream();
-  if (PyLong_Check(stream.ptr())) return reinterpret_cast<hipStream_t>(py::cast<uintptr_t>(stream));
-  return reinterpret_cast<hipStream_t>(py::cast<uintptr_t>(stream.attr("cuda_stream")));
+c10::hip::HIPStream stream_of(const py::object& stream, at::Device device) {
+  if (stream.is_none()) return c10::hip::getCurrentHIPStream(device.index());
+  const uintptr_t handle = PyLong_Check(stream.ptr()) ? py::cast<uintptr_t>(stream)
+                                                      : py::cast<uintptr_t>(stream.attr("cuda_stream"));
+  return c10::hip::getStreamFromExternal(reinterpret_cast<hipStream_t>(handle), device.index());
+}
+
+// A tensor that a call on `stream` makes for itself.  The allocator orders
+// the use of a block on the stream that was current when it was handed out
+// alone: one from another stream's pool may still be in use there when the
+// call writes it, and handed out there again while the call still works.
+Tensor made_on(at::IntArrayRef sizes, const at::TensorOptions& options, c10::hip::HIPStream stream) {
+  const c10::hip::HIPStream before = c10::hip::getCurrentHIPStream(stream.device_index());
+  if (before.stream() == stream.stream()) return at::empty(sizes, options);
+  struct Current {
+    c10::hip::HIPStream before;
+    ~Current() { c10::hip::setCurrentHIPStream(before); }
+  } restore{before};
+  c10::hip::setCurrentHIPStream(stream);
+  return at::empty(sizes, options);
 }
 
 int32_t small(int64_t x, const char* what) {
@@ -162,6 +178,7 @@ py::tuple plan_step(const Tensor& kv_len, const Tensor& new_tokens, const Tensor
                     const py::object& stream) {
   OneGpu on("plan_step");
   on(kv_len)(new_tokens)(block_table)(free_blocks)(free_count);
+  const auto at_stream = stream_of(stream, on.device());
   const int64_t R = kv_len.numel();
   need(n_tokens >= 0, "n_tokens must not be negative");
   std::vector<Tensor> o;
@@ -171,8 +188,9 @@ py::tuple plan_step(const Tensor& kv_len, const Tensor& new_tokens, const Tensor
     for (const Tensor& t : o) on(t);
   } else {
     const auto i32 = kv_len.options().dtype(at::kInt);
-    o = {at::empty({R}, i32), at::empty({R + 1}, i32), at::empty({n_tokens}, i32),
-         at::empty({n_tokens}, i32.dtype(at::kLong)), at::empty({R}, i32), at::empty({1}, i32)};
+    const auto ints_of = [&](int64_t n) { return made_on({n}, i32, at_stream); };
+    o = {ints_of(R), ints_of(R + 1), ints_of(n_tokens),
+         made_on({n_tokens}, i32.dtype(at::kLong), at_stream), ints_of(R), ints_of(1)};
   }
   const Tensor &len_out = o[0], &q_start = o[1], &positions = o[2], &slots = o[3], &refused = o[4],
                &count_out = o[5];
@@ -202,7 +220,7 @@ py::tuple plan_step(const Tensor& kv_len, const Tensor& new_tokens, const Tensor
   s.positions = ints(positions, "positions");
   s.slots = static_cast<int64_t*>(slots.data_ptr());
   s.refused = ints(refused, "refused");
-  const int st = calls.plan(&s, stream_of(stream, on.device()));
+  const int st = calls.plan(&s, at_stream.stream());
   return py::make_tuple(st, o[0], o[1], o[2], o[3], o[4], o[5]);
 }
 
@@ -211,6 +229,7 @@ py::tuple rope_heads(const Tensor& q, const Maybe& k, const Tensor& positions, u
                      bool inverse, const Maybe& q_out, const Maybe& k_out, const py::object& stream) {
   OneGpu on("rope_heads");
   on(q)(k)(positions)(q_out)(k_out);
+  const auto at_stream = stream_of(stream, on.device());
   const auto* a = reinterpret_cast<const hkv_rope_axes*>(axes);
   const hkv_heads qh = heads_of(q, "q");
   const int64_t n = q.size(0);
@@ -218,13 +237,13 @@ py::tuple rope_heads(const Tensor& q, const Maybe& k, const Tensor& positions, u
   if ((positions.dim() != 1 && positions.dim() != 2) || positions.scalar_type() != at::kInt ||
       rows != a->n_axes || positions.size(-1) != n || (n > 1 && positions.stride(-1) != 1))
     refuse("positions must be int32 [" + std::to_string(a->n_axes) + ", n_tokens], last axis contiguous");
-  const Tensor qo = q_out ? *q_out : at::empty(q.sizes(), q.options());
+  const Tensor qo = q_out ? *q_out : made_on(q.sizes(), q.options(), at_stream);
   const hkv_heads qoh = heads_of(qo, "q_out");
   hkv_heads kh = {}, koh = {};
   Maybe ko = k_out;
   bool same = qo.sizes() == q.sizes() && qo.scalar_type() == q.scalar_type();
   if (k) {
-    if (!ko) ko = at::empty(k->sizes(), k->options());
+    if (!ko) ko = made_on(k->sizes(), k->options(), at_stream);
     kh = heads_of(*k, "k");
     koh = heads_of(*ko, "k_out");
     same = same && k->size(0) == n && ko->sizes() == k->sizes() &&
@@ -233,7 +252,7 @@ py::tuple rope_heads(const Tensor& q, const Maybe& k, const Tensor& positions, u
   need(same, "q, k and their outputs must share dtype and n_tokens, each output its input's shape");
   const int st = calls.rope(a, static_cast<const int32_t*>(positions.data_ptr()),
                             rows > 1 ? positions.stride(0) : 0, small(n, "n_tokens"), &qh, &kh, &qoh,
-                            &koh, dtype_of(q), inverse ? 1 : 0, stream_of(stream, on.device()));
+                            &koh, dtype_of(q), inverse ? 1 : 0, at_stream.stream());
   return py::make_tuple(st, qo, ko);
 }
 
@@ -248,7 +267,7 @@ int append_tokens(const Tensor& k, const Tensor& v, const Tensor& slots, const T
   const Pool pool = pool_of(records, fmt, block_tokens, k.size(1));
   return calls.append(&pool.shape, fmt, &kh, &vh, dtype_of(k), small(k.size(0), "n_tokens"),
                       static_cast<const int64_t*>(slots.data_ptr()), &pool.records,
-                      stream_of(stream, on.device()));
+                      stream_of(stream, on.device()).stream());
 }
 
 // workspace: True (made here where one is needed), None or a uint8 tensor.
@@ -264,6 +283,7 @@ py::tuple attend_records(const Tensor& q, const Tensor& records, int fmt, int64_
   const bool make = workspace.is(py::bool_(true));
   if (!make && !workspace.is_none()) ws = py::cast<Tensor>(workspace);
   on(ws);
+  const auto at_stream = stream_of(stream, on.device());
   const hkv_heads qh = heads_of(q, "q");
   const int64_t n = q.size(0), hq = q.size(1);
   const Table table = table_of(block_table);
@@ -271,9 +291,9 @@ py::tuple attend_records(const Tensor& q, const Tensor& records, int fmt, int64_
   need(kv_len.numel() == R && (q_start ? q_start->numel() == R + 1 : n == R),
        "kv_len [n_requests], q_start [n_requests + 1] (or one query per request) and block_table must agree");
   if (max_queries < 0) max_queries = q_start ? (n > 1 ? n : 1) : 1;
-  const Tensor out = out_ ? *out_ : at::empty(q.sizes(), q.options());
+  const Tensor out = out_ ? *out_ : made_on(q.sizes(), q.options(), at_stream);
   need(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type(), "out must have q's shape and dtype");
-  const Tensor lse = lse_ ? *lse_ : at::empty({n, hq}, q.options().dtype(at::kFloat));
+  const Tensor lse = lse_ ? *lse_ : made_on({n, hq}, q.options().dtype(at::kFloat), at_stream);
   need(lse.dim() == 2 && lse.size(0) == n && lse.size(1) == hq && lse.scalar_type() == at::kFloat &&
            lse.is_contiguous(),
        "lse must be a contiguous float32 [n_tokens, n_q_heads] tensor");
@@ -291,24 +311,14 @@ py::tuple attend_records(const Tensor& q, const Tensor& records, int fmt, int64_
   const int dtype = dtype_of(q);
   if (make) {
     const int64_t bytes = calls.attend_bytes(&pool.shape, &req, small(n, "n_tokens"), qh.n_heads, dtype);
-    if (bytes > 0) {
-      ws = at::empty({bytes}, q.options().dtype(at::kByte));
-      // the allocator hands it out again only when the call's stream is done
-      if (!stream.is_none()) {
-        const py::object on_stream =
-            PyLong_Check(stream.ptr())
-                ? py::module_::import("torch").attr("cuda").attr("ExternalStream")(stream, py::cast(on.device()))
-                : stream;
-        py::cast(*ws).attr("record_stream")(on_stream);
-      }
-    }
+    if (bytes > 0) ws = made_on({bytes}, q.options().dtype(at::kByte), at_stream);
   }
   if (ws) need(ws->scalar_type() == at::kByte && ws->is_contiguous(), "workspace must be a contiguous uint8 tensor");
   const hkv_heads oh = heads_of(out, "out");
   const int st = calls.attend(&pool.shape, fmt, &pool.records, &req, &qh, dtype, small(n, "n_tokens"),
                               sm_scale, causal ? 1 : 0, delta_m ? &shift : nullptr, &oh,
                               static_cast<float*>(lse.data_ptr()), ws ? ws->data_ptr() : nullptr,
-                              ws ? ws->numel() : 0, stream_of(stream, on.device()));
+                              ws ? ws->numel() : 0, at_stream.stream());
   return py::make_tuple(st, out, lse);
 }
 
@@ -343,7 +353,7 @@ int fetch(bool per_token, const Tensor& records, int fmt, const Tensor& block_ta
   const int32_t* order = visit_order ? ints(*visit_order, "visit_order") : nullptr;
   return (per_token ? calls.fetch_tokens : calls.fetch)(
       &shape, fmt, &rec, ints(block_table, "block_table"), ints(delta, "delta_m"), order, rope_base,
-      pairs, &pages, dtype_of(k), stream_of(stream, on.device()));
+      pairs, &pages, dtype_of(k), stream_of(stream, on.device()).stream());
 }
 
 }  // namespace

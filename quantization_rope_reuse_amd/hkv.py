@@ -4,7 +4,8 @@ csrc/binding.cpp for the fetch and the serving calls.
 Argument marshalling only: every step of put, CRC and fetch runs in the HIP
 kernels of libhkv.so.  torch is used for device memory and streams: tensors
 supply device pointers and strides, and calls are enqueued on the caller's
-current torch stream unless another is given.
+current torch stream unless another is given.  What a serving call makes for
+itself (outputs left as None, a workspace) is made for the call's stream.
 
 There is no fallback: if libhkv.so or the native part is missing or cannot be
 loaded, the calls raise.
