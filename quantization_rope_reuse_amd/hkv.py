@@ -4,8 +4,8 @@ csrc/binding.cpp for the fetch and the serving calls.
 Argument marshalling only: every step of put, CRC and fetch runs in the HIP
 kernels of libhkv.so.  torch is used for device memory and streams: tensors
 supply device pointers and strides, and calls are enqueued on the caller's
-current torch stream unless another is given.  What a serving call makes for
-itself (outputs left as None, a workspace) is made for the call's stream.
+current torch stream unless another is given.  What a call makes for itself
+(outputs left as None, a workspace) is made for the call's stream.
 
 There is no fallback: if libhkv.so or the native part is missing or cannot be
 loaded, the calls raise.
@@ -246,6 +246,20 @@ def _stream(stream, device):
     return ctypes.c_void_p(int(stream))
 
 
+def _made_on(stream, size, dtype, device):
+    """An empty tensor that a call on `stream` makes for itself.  The allocator
+    orders the use of a block on the stream that was current when it was handed
+    out alone, so the call's stream has to be."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # (a handle of 0 is the default stream; ExternalStream would make a new one)
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
+            else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
 def _as5d(t: torch.Tensor) -> torch.Tensor:
     """Pages as [L, P, T_b, H, 128]; a 4-D tensor is one layer."""
     if t.dim() == 4:
@@ -372,12 +386,12 @@ def quant_crc(fmt, k_pages, v_pages, block_table, records, crc_out=None, workspa
     if records.shape[0] != L or records.shape[1] != nb:
         raise ValueError("records must be [L, n_blocks, bytes] matching pages and table")
     if crc_out is None:
-        crc_out = torch.empty((L, nb), dtype=torch.int32, device=records.device)
+        crc_out = _made_on(stream, (L, nb), torch.int32, records.device)
     if crc_out.dtype != torch.int32 or not crc_out.is_contiguous() or crc_out.numel() != L * nb:
         raise ValueError("crc_out must be a contiguous int32 tensor of L * n_blocks elements")
     need = quant_crc_workspace_bytes(fmt, L, nb, tb, H)
     if workspace is True:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=records.device)
+        workspace = _made_on(stream, max(need, 16), torch.uint8, records.device)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     shape = Shape(L, nb, tb, H, d)
@@ -534,7 +548,7 @@ def page_visit_order(block_table, num_pages: int, out=None, stream=None):
     an int32 tensor [n_blocks] for fetch_dequant_rope_shift's visit_order."""
     nb = block_table.numel()
     if out is None:
-        out = torch.empty(nb, dtype=torch.int32, device=block_table.device)
+        out = _made_on(stream, nb, torch.int32, block_table.device)
     if out.numel() != nb:
         raise ValueError("out must hold n_blocks entries")
     st = lib().hkv_page_visit_order(_i32(block_table, "block_table"), nb, int(num_pages),
@@ -569,7 +583,7 @@ def crc32_blocks(records, fmt, block_tokens: int, n_kv_heads: int, out=None, str
     (use `.view(torch.uint32)` or mask with 0xFFFFFFFF after widening)."""
     L, nb = records.shape[0], records.shape[1]
     if out is None:
-        out = torch.empty((L, nb), dtype=torch.int32, device=records.device)
+        out = _made_on(stream, (L, nb), torch.int32, records.device)
     if out.dtype != torch.int32 or not out.is_contiguous() or out.numel() != L * nb:
         raise ValueError("out must be a contiguous int32 tensor of L * n_blocks elements")
     shape = Shape(L, nb, block_tokens, n_kv_heads, HEAD_DIM)
@@ -593,7 +607,7 @@ def token_drift(h_cached, h_fresh, out=None, stream=None):
         raise ValueError("hidden states must share row strides, last axis contiguous")
     n, d = h_cached.shape
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=h_cached.device)
+        out = _made_on(stream, n, torch.float32, h_cached.device)
     if out.dtype != torch.float32 or not out.is_contiguous() or out.numel() != n:
         raise ValueError("out must be a contiguous float32 tensor of n_tokens elements")
     st = lib().hkv_token_drift(ctypes.c_void_p(h_cached.data_ptr()),
@@ -618,12 +632,11 @@ def select_top_tokens(drift, k: int, out=None, workspace=True, stream=None):
         raise ValueError("drift must be a contiguous float32 tensor")
     n = drift.numel()
     if out is None:
-        out = torch.empty(max(int(k), 0), dtype=torch.int32, device=drift.device)
+        out = _made_on(stream, max(int(k), 0), torch.int32, drift.device)
     if out.numel() < k:
         raise ValueError("out must hold k entries")
     if workspace is True:
-        workspace = torch.empty(max(select_workspace_bytes(n), 16), dtype=torch.uint8,
-                                device=drift.device)
+        workspace = _made_on(stream, max(select_workspace_bytes(n), 16), torch.uint8, drift.device)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None and workspace is not False:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -687,7 +700,7 @@ def frame_verify(frames, fmt, block_tokens: int, n_kv_heads: int, layer_base: in
     shape, fr = _frame_args(frames, fmt, block_tokens, n_kv_heads)
     L, nb = frames.shape[0], frames.shape[1]
     if out is None:
-        out = torch.empty((L, nb), dtype=torch.int32, device=frames.device)
+        out = _made_on(stream, (L, nb), torch.int32, frames.device)
     if out.numel() != L * nb:
         raise ValueError("out must hold L * n_blocks entries")
     st = lib().hkv_frame_verify(ctypes.byref(shape), FORMATS[fmt], ctypes.byref(fr),
@@ -704,7 +717,7 @@ def frame_delta_m(frames, fmt, block_tokens: int, n_kv_heads: int, m_new, out=No
     shape, fr = _frame_args(frames, fmt, block_tokens, n_kv_heads)
     nb = frames.shape[1]
     if out is None:
-        out = torch.empty(nb, dtype=torch.int32, device=frames.device)
+        out = _made_on(stream, nb, torch.int32, frames.device)
     if out.numel() != nb or m_new.numel() != nb:
         raise ValueError("m_new and out must hold n_blocks entries")
     st = lib().hkv_frame_delta_m(ctypes.byref(shape), FORMATS[fmt], ctypes.byref(fr),

@@ -92,3 +92,38 @@ def test_current_stream_busy_with_freed_memory(handle):
     torch.cuda.synchronize()
     for out, (a, b) in zip(outs, kept):
         assert torch.equal(out, want) and torch.equal(a, want) and torch.equal(b, want_lse)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_cache_calls_make_on_their_stream(handle):
+    """The same for the put with CRC, the CRC, the page order, the selection
+    and the frames; results as on the current stream."""
+    tb, h, nb = 64, 2, 8
+    k, v = (torch.randn(1, nb, tb, h, 128, device=DEV).bfloat16() for _ in range(2))
+    table = torch.arange(nb - 1, -1, -1, dtype=torch.int32, device=DEV)
+    rec = hkv.alloc_records(1, nb, "fp8", tb, h, device=DEV)
+    frames = hkv.alloc_frames(1, nb, "fp8", tb, h, device=DEV)
+    x, y = (torch.randn(5000, 64, device=DEV) for _ in range(2))
+
+    def calls(**kw):
+        made = [hkv.quant_crc("fp8", k, v, table, rec, **kw), hkv.crc32_blocks(rec, "fp8", tb, h, **kw),
+                hkv.page_visit_order(table, nb, **kw)]
+        made.append(hkv.token_drift(x, y, **kw))
+        made.append(hkv.select_top_tokens(made[-1], 100, **kw))
+        hkv.quant_fp8(k, v, table, hkv.frame_records(frames), **kw)
+        hkv.frame_headers(frames, "fp8", tb, h, made[0], table, **kw)
+        made += [hkv.frame_verify(frames, "fp8", tb, h, **kw), hkv.frame_delta_m(frames, "fp8", tb, h, table, **kw)]
+        return made
+    want = calls()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    before = reserved(0)
+    got = calls(stream=side.cuda_stream if handle else side)
+    assert [pool_stream(t) for t in got] == [side.cuda_stream] * len(got)
+    assert reserved(0) == before         # workspaces included
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.cuda.stream(side):
+        assert pool_stream(hkv.crc32_blocks(rec, "fp8", tb, h, stream=0)) == 0
+    torch.cuda.synchronize()
