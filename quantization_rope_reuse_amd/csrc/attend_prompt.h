@@ -208,6 +208,7 @@ void attend_prompt_kernel(AttendParams p) {
 
     f32x16 o[4] = {};
     float m = kNoReference, l = 0.0f;
+    bool far = false;                      // some row's reference is (kFar)
 
     // What this thread brings of a tile: 16 dims of a token's key, 8 dims of
     // two tokens' values (the pairs of a wave fill one chunk); waves 0 and 1 a
@@ -441,12 +442,20 @@ void attend_prompt_kernel(AttendParams p) {
             }
           };
           auto weights = [&]() __attribute__((always_inline)) {
-            const float shift = 14.0f - m;
+            if (far) {
+              // the reference came from rounded scores: so do the weights
+#pragma clang fp contract(off)
+              const float unit = fabsf(m) < kFar ? 14.0f : -3.0f;
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-              const f32x4 k4 = *reinterpret_cast<const f32x4*>(ks + 4 * a);
+              for (int i = 0; i < 16; ++i) w[i] = (acc[i] * ks[i] - m) + unit;
+            } else {
+              const float shift = 14.0f - m;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) w[4 * a + i] = __builtin_fmaf(acc[4 * a + i], k4[i], shift);
+              for (int a = 0; a < 4; ++a) {
+                const f32x4 k4 = *reinterpret_cast<const f32x4*>(ks + 4 * a);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[4 * a + i] = __builtin_fmaf(acc[4 * a + i], k4[i], shift);
+              }
             }
             if (part) {
 #pragma unroll
@@ -501,7 +510,7 @@ void attend_prompt_kernel(AttendParams p) {
             for (int i = 0; i < 16; ++i) {
               const float s2 = acc[i] * ks[i];
               const float lv = fminf(__builtin_amdgcn_logf(fabsf(vs[i])), 16.0f);
-              const float x = fmaxf(s2 + lv, s2 - 80.0f);
+              const float x = fabsf(s2) < kFar ? fmaxf(s2 + lv, s2 - 80.0f) : s2;
               want = fmaxf(want, (vis >> i) & 1 ? x : kNoReference);
               if ((i & 7) == 7) __builtin_amdgcn_sched_barrier(0);    // few registers at a time
             }
@@ -509,6 +518,7 @@ void attend_prompt_kernel(AttendParams p) {
             const float m_new = fmaxf(m, rintf(want) + 1.0f);
             const float keep = m == m_new ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
             m = m_new;
+            far = __any(fabsf(m) >= kFar && m > kNoReference);
             l *= keep;
 #pragma unroll
             for (int d = 0; d < 4; ++d)

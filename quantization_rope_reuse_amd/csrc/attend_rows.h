@@ -161,6 +161,14 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 constexpr float kWeightScale = 0x1p14f;
 
+// From here on a reference has no bits for log2(v_scale) or for 14 beside a
+// score, and moves by steps of its own: it takes the largest score alone, and
+// weights are 2^-17 of the usual, which keeps them in fp16 whatever v_scale
+// is (below 2^16).  Terms of one row that differ by those 2^17 are no further
+// apart than scores of this size are exact.
+constexpr float kFar = 0x1p23f;
+constexpr float kFarBits = 17.0f;
+
 // log(2^m l), m a whole number; -infinity for l = 0.  Only the logarithm of
 // l's significand is rounded before the last sum.
 __device__ __forceinline__ float log_sum(float m, float l) {
@@ -684,11 +692,11 @@ void attend_rows_kernel(AttendParams p) {
       }
       h8 pf[NT][PP];
       auto weights = [&](float (&w)[8], const float (&sv)[8], int n,
-                         float* sum) __attribute__((always_inline)) {
+                         float* sum, float less) __attribute__((always_inline)) {
         float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[i], grow[n], -st.m[n]));
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[i], grow[n], -st.m[n]) - less);
           total += e;
           w[i] = e * vs[i];
         }
@@ -714,7 +722,7 @@ void attend_rows_kernel(AttendParams p) {
             sv[n][i] = vis ? sv[n][i] : -INFINITY;
           }
         }
-        weights(w[n], sv[n], n, &sum[n]);
+        weights(w[n], sv[n], n, &sum[n], 0.0f);
         // a token that the row does not see weighs nothing whatever its scale
         if (part) {
 #pragma unroll
@@ -756,7 +764,7 @@ void attend_rows_kernel(AttendParams p) {
           for (int i = 0; i < 8; ++i) {
             const float s2 = sv[n][i] * grow[n];
             const float lv = fminf(__builtin_amdgcn_logf(fabsf(vs[i])) - 14.0f, 16.0f);
-            want = fmaxf(want, fmaxf(s2 + lv, s2 - 80.0f));
+            want = fmaxf(want, fabsf(s2) < kFar ? fmaxf(s2 + lv, s2 - 80.0f) : s2);
           }
           want = fmaxf(want, __shfl_xor(want, 16));
           want = fmaxf(want, __shfl_xor(want, 32));
@@ -768,7 +776,7 @@ void attend_rows_kernel(AttendParams p) {
           for (int d = 0; d < 8; ++d)
 #pragma unroll
             for (int i = 0; i < 4; ++i) st.o[n][d][i] *= keep;
-          weights(w[n], sv[n], n, &sum[n]);
+          weights(w[n], sv[n], n, &sum[n], fabsf(m) < kFar ? 0.0f : kFarBits);
           if (part) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[n][i] = sv[n][i] == -INFINITY ? 0.0f : w[n][i];
