@@ -125,7 +125,9 @@ void attend_prompt_kernel(AttendParams p) {
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
     }
     top = fmaxf(top, __shfl_xor(top, 32));
-    float most = top, least = top > 0.0f ? top : INFINITY;
+    // (A row that is not finite counts for neither: it has a power of its own.)
+    const bool finite = top < INFINITY;
+    float most = finite ? top : 0.0f, least = finite && top > 0.0f ? top : INFINITY;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       most = fmaxf(most, __shfl_xor(most, off));
@@ -146,8 +148,8 @@ void attend_prompt_kernel(AttendParams p) {
       return t > 0.0f && t < INFINITY ? max(__builtin_amdgcn_frexp_expf(t) - 14, -100) : 0;
     };
     const int e_all = __builtin_amdgcn_readfirstlane(power(most));
-    const bool uneven = __builtin_amdgcn_readfirstlane(
-        most < INFINITY && least < INFINITY && power(least) < e_all - 14);
+    const bool uneven = __any(!finite) ||
+                        __builtin_amdgcn_readfirstlane(least < INFINITY && power(least) < e_all - 14);
     const int e_row = uneven ? power(top) : e_all;
     const float even_out = __builtin_ldexpf(1.0f, e_row - e_all);
     const float ks_scale = p.scale_log2 * __builtin_ldexpf(1.0f, e_all);
