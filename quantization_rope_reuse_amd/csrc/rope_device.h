@@ -49,12 +49,12 @@ __device__ __forceinline__ int lane_pair(int pairs, int sub, int j) {
   return 8 * sub + j;
 }
 
-// (a, b) turned by the angle whose cosine and sine are c and s; a pair that
-// does not turn (s = 0 only for an angle of 0, where c = 1) keeps its values
+// (a, b) turned by the angle whose cosine and sine are c and s.  s = 0 only
+// for whole half turns, where c = 1 or -1: either value then keeps its size
 // whatever its partner holds.
 __device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-  const float x = s == 0.0f ? a : a * c - b * s;
-  const float y = s == 0.0f ? b : a * s + b * c;
+  const float x = s == 0.0f ? a * c : a * c - b * s;
+  const float y = s == 0.0f ? b * c : a * s + b * c;
   a = x;
   b = y;
 }
