@@ -76,9 +76,12 @@ class OneGpu {
 
 c10::hip::HIPStream stream_of(const py::object& stream, at::Device device) {
   if (stream.is_none()) return c10::hip::getCurrentHIPStream(device.index());
-  const uintptr_t handle = PyLong_Check(stream.ptr()) ? py::cast<uintptr_t>(stream)
-                                                      : py::cast<uintptr_t>(stream.attr("cuda_stream"));
-  return c10::hip::getStreamFromExternal(reinterpret_cast<hipStream_t>(handle), device.index());
+  // a torch stream, or a handle: any whole number
+  const py::object handle =
+      PyIndex_Check(stream.ptr()) ? stream : py::getattr(stream, "cuda_stream", py::none());
+  if (!PyIndex_Check(handle.ptr())) refuse("stream must be a torch stream or a stream's handle");
+  const uintptr_t at = py::cast<uintptr_t>(py::reinterpret_steal<py::object>(PyNumber_Index(handle.ptr())));
+  return c10::hip::getStreamFromExternal(reinterpret_cast<hipStream_t>(at), device.index());
 }
 
 // A tensor that a call on `stream` makes for itself.  The allocator orders

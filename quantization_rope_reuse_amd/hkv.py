@@ -453,7 +453,7 @@ def fetch_dequant_rope_shift(records, fmt, block_table, delta_m, rope_base, pair
     """Dequantize records[:, b], shift keys by delta_m[b], store at page
     block_table[b] of k/v_pages (dtype of the pages).  visit_order: optional
     int32 permutation of the blocks (see page_visit_order)."""
-    st = native().fetch(False, records, FORMATS[fmt], block_table, delta_m, rope_base,
+    st = native().fetch(False, records, FORMATS[fmt], block_table, delta_m, float(rope_base),
                         PAIRS[pairs], k_pages, v_pages, visit_order, stream)
     _check("hkv_fetch_dequant_rope_shift", st)
     return k_pages, v_pages
@@ -463,8 +463,8 @@ def fetch_dequant_rope_shift_tokens(records, fmt, block_table, delta_m_tokens, r
                                     k_pages, v_pages, visit_order=None, stream=None):
     """As fetch_dequant_rope_shift with one delta per token: delta_m_tokens
     is an int32 [n_blocks, block_tokens] tensor."""
-    st = native().fetch(True, records, FORMATS[fmt], block_table, delta_m_tokens, rope_base,
-                        PAIRS[pairs], k_pages, v_pages, visit_order, stream)
+    st = native().fetch(True, records, FORMATS[fmt], block_table, delta_m_tokens,
+                        float(rope_base), PAIRS[pairs], k_pages, v_pages, visit_order, stream)
     _check("hkv_fetch_dequant_rope_shift_tokens", st)
     return k_pages, v_pages
 
