@@ -47,6 +47,14 @@ void bind(const py::dict& at) {
   set(calls.record_bytes, "hkv_record_bytes");
 }
 
+// A library call, without the interpreter's lock: a launch waits where the
+// stream's queue is full.
+template <class Call, class... Args>
+int launch(Call call, Args... args) {
+  py::gil_scoped_release unlocked;
+  return call(args...);
+}
+
 [[noreturn]] void refuse(const std::string& what) { throw py::value_error(what); }
 
 void need(bool ok, const char* what) {
@@ -223,7 +231,7 @@ py::tuple plan_step(const Tensor& kv_len, const Tensor& new_tokens, const Tensor
   s.positions = ints(positions, "positions");
   s.slots = static_cast<int64_t*>(slots.data_ptr());
   s.refused = ints(refused, "refused");
-  const int st = calls.plan(&s, at_stream.stream());
+  const int st = launch(calls.plan, &s, at_stream.stream());
   return py::make_tuple(st, o[0], o[1], o[2], o[3], o[4], o[5]);
 }
 
@@ -253,9 +261,9 @@ py::tuple rope_heads(const Tensor& q, const Maybe& k, const Tensor& positions, u
            k->scalar_type() == q.scalar_type() && ko->scalar_type() == q.scalar_type();
   }
   need(same, "q, k and their outputs must share dtype and n_tokens, each output its input's shape");
-  const int st = calls.rope(a, static_cast<const int32_t*>(positions.data_ptr()),
-                            rows > 1 ? positions.stride(0) : 0, small(n, "n_tokens"), &qh, &kh, &qoh,
-                            &koh, dtype_of(q), inverse ? 1 : 0, at_stream.stream());
+  const int st = launch(calls.rope, a, static_cast<const int32_t*>(positions.data_ptr()),
+                        rows > 1 ? positions.stride(0) : 0, small(n, "n_tokens"), &qh, &kh, &qoh,
+                        &koh, dtype_of(q), inverse ? 1 : 0, at_stream.stream());
   return py::make_tuple(st, qo, ko);
 }
 
@@ -268,9 +276,9 @@ int append_tokens(const Tensor& k, const Tensor& v, const Tensor& slots, const T
   need(slots.scalar_type() == at::kLong && slots.is_contiguous() && slots.numel() == k.size(0),
        "slots must be a contiguous int64 tensor of n_tokens elements");
   const Pool pool = pool_of(records, fmt, block_tokens, k.size(1));
-  return calls.append(&pool.shape, fmt, &kh, &vh, dtype_of(k), small(k.size(0), "n_tokens"),
-                      static_cast<const int64_t*>(slots.data_ptr()), &pool.records,
-                      stream_of(stream, on.device()).stream());
+  return launch(calls.append, &pool.shape, fmt, &kh, &vh, dtype_of(k), small(k.size(0), "n_tokens"),
+                static_cast<const int64_t*>(slots.data_ptr()), &pool.records,
+                stream_of(stream, on.device()).stream());
 }
 
 // workspace: True (made here where one is needed), None or a uint8 tensor.
@@ -318,10 +326,10 @@ py::tuple attend_records(const Tensor& q, const Tensor& records, int fmt, int64_
   }
   if (ws) need(ws->scalar_type() == at::kByte && ws->is_contiguous(), "workspace must be a contiguous uint8 tensor");
   const hkv_heads oh = heads_of(out, "out");
-  const int st = calls.attend(&pool.shape, fmt, &pool.records, &req, &qh, dtype, small(n, "n_tokens"),
-                              sm_scale, causal ? 1 : 0, delta_m ? &shift : nullptr, &oh,
-                              static_cast<float*>(lse.data_ptr()), ws ? ws->data_ptr() : nullptr,
-                              ws ? ws->numel() : 0, at_stream.stream());
+  const int st = launch(calls.attend, &pool.shape, fmt, &pool.records, &req, &qh, dtype,
+                        small(n, "n_tokens"), sm_scale, causal ? 1 : 0,
+                        delta_m ? &shift : nullptr, &oh, static_cast<float*>(lse.data_ptr()),
+                        ws ? ws->data_ptr() : nullptr, ws ? ws->numel() : 0, at_stream.stream());
   return py::make_tuple(st, out, lse);
 }
 
@@ -354,9 +362,9 @@ int fetch(bool per_token, const Tensor& records, int fmt, const Tensor& block_ta
   const hkv_pages pages = {k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
                            k.stride(3), small(k.size(1), "num_pages")};
   const int32_t* order = visit_order ? ints(*visit_order, "visit_order") : nullptr;
-  return (per_token ? calls.fetch_tokens : calls.fetch)(
-      &shape, fmt, &rec, ints(block_table, "block_table"), ints(delta, "delta_m"), order, rope_base,
-      pairs, &pages, dtype_of(k), stream_of(stream, on.device()).stream());
+  return launch(per_token ? calls.fetch_tokens : calls.fetch, &shape, fmt, &rec,
+                ints(block_table, "block_table"), ints(delta, "delta_m"), order, rope_base, pairs,
+                &pages, dtype_of(k), stream_of(stream, on.device()).stream());
 }
 
 }  // namespace

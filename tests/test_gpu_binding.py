@@ -1,5 +1,8 @@
-"""The native part of the binding: what it takes for a stream and a base."""
+"""The native part of the binding: what it takes for a stream and a base, and
+the interpreter's lock, which no library call holds."""
 from __future__ import annotations
+
+import ctypes
 
 import numpy as np
 import pytest
@@ -52,3 +55,16 @@ def test_fetch_takes_what_float_takes():
     for base in (torch.tensor(1e4), np.float32(1e4), "1e4", 10000):
         f(*args[:4], base, *args[5:])
     torch.cuda.synchronize()
+
+@pytest.mark.parametrize("call", list(hkv.NATIVE_CALLS[:4] + hkv.NATIVE_CALLS[5:7]))
+def test_calls_release_the_interpreter(call):
+    """PyGILState_Check in the library call's place: 1, an unknown status, if
+    the calling thread holds the lock."""
+    f, args = arguments()[call]
+    at = {n: ctypes.cast(getattr(hkv.lib(), n), ctypes.c_void_p).value for n in hkv.NATIVE_CALLS}
+    check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    try:
+        hkv.native().bind({**at, call: check})
+        f(*args)
+    finally:
+        hkv.native().bind(at)
