@@ -789,7 +789,6 @@ def plan_step(kv_len, new_tokens, block_table, free_blocks, free_count, block_to
     return StepPlan(*plan) if out is None else out
 
 
-@functools.lru_cache(maxsize=64)
 def rope_axes(rope_base: float, pairs, sections=(HEAD_DIM // 2,), order="blocked", freq=None):
     """The axes of rope_heads.  sections: pairs per axis, at most 64 in all;
     the rest do not turn.  order: "blocked" gives each axis a run of pairs,
