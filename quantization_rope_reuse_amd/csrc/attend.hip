@@ -263,6 +263,7 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     const dim3 grid = per_request(static_cast<int64_t>(c.g.n_heads) * share.splits);
     e = c.fmt == kFP8 ? launch_prompt_fp8(p, grid, stream) : launch_prompt_int4(p, grid, stream);
   } else {
+    // at most 44 KB of LDS (the prefix sums of kMaxFlatRequests requests: 4)
     size_t bytes = kRowsWaves * kWaveAreaBytes + (kRowsWaves / 2) * share.nt * (8192 + 512);
     if (share.ranges > 0) bytes += static_cast<size_t>(prefix_bytes(c.req));
     const dim3 grid = share.ranges > 0 ? dim3(static_cast<unsigned>(share.ranges * share.head_sets))

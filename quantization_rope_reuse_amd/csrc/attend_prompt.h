@@ -87,7 +87,6 @@ void attend_prompt_kernel(AttendParams p) {
   const Span s = span_of(p, r);
   const int row_tiles = (s.rows + kPromptRows - 1) / kPromptRows;
   const int step = gridDim.x / (p.n_heads * p.splits);
-  const int64_t token_bytes = static_cast<int64_t>(p.n_heads) * CB;
   const int64_t v_off = static_cast<int64_t>(p.vecs) * CB;
   const int32_t* table = p.table + r * p.table_stride;
   const int32_t* moves = p.delta ? p.delta + r * p.table_stride : nullptr;

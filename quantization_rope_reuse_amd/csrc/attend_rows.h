@@ -935,13 +935,6 @@ void attend_rows_kernel(AttendParams p) {
 template <int FMT, int DT, int HP, int NT, int QP>
 hipError_t launch_rows_tiles(const AttendParams& p, dim3 grid, size_t bytes, hipStream_t stream) {
   auto go = [&](auto* kernel) {
-    // more than 64 KB of LDS has to be asked for
-    if (bytes > 65536) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(bytes));
-      if (e != hipSuccess) return e;
-    }
     hipLaunchKernelGGL(kernel, grid, dim3(kRowsThreads), bytes, stream, p);
     return hipGetLastError();
   };
@@ -954,19 +947,21 @@ hipError_t launch_rows_tiles(const AttendParams& p, dim3 grid, size_t bytes, hip
 template <int FMT, int DT>
 hipError_t launch_rows_dtype(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                              hipStream_t stream) {
-  if (DT == kF32 || p.delta) {
-    // two parts per query: 32 rows of them leave the registers, and 16 rows
-    // twice over are faster (58 against 132 us for drafts of five tokens of 16
-    // requests over FP8 records)
+  // two parts per query: 32 rows of them leave the registers, and 16 rows
+  // twice over are faster (58 against 132 us for drafts of five tokens of 16
+  // requests over FP8 records)
+  auto two_parts = [&] {
     return hp == 2 ? launch_rows_tiles<FMT, DT, 2, 1, 2>(p, grid, bytes, stream)
                    : launch_rows_tiles<FMT, DT, 1, 1, 2>(p, grid, bytes, stream);
-  }
-  if constexpr (DT != kF32) {
+  };
+  if constexpr (DT == kF32) {
+    return two_parts();
+  } else {
+    if (p.delta) return two_parts();
     if (hp == 2) return launch_rows_tiles<FMT, DT, 2, 1, 1>(p, grid, bytes, stream);
     return nt == 1 ? launch_rows_tiles<FMT, DT, 1, 1, 1>(p, grid, bytes, stream)
                    : launch_rows_tiles<FMT, DT, 1, 2, 1>(p, grid, bytes, stream);
   }
-  return hipErrorInvalidValue;           // not reached
 }
 
 template <int FMT>
