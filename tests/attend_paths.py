@@ -1,7 +1,14 @@
-"""Attention calls that reach every way the rows kernel shares out its work:
+"""Attention calls that reach every way the work is shared out.
+
+cases(): the rows kernel's,
 (name, format, dtype, block_tokens, key heads, query heads per key head,
 lengths, queries, moved, expected share).  A share is (heads per score tile,
-tiles of 16 rows, heads of different waves of a workgroup, cut into ranges)."""
+tiles of 16 rows, heads of different waves of a workgroup, cut into ranges).
+
+PROMPTS: the prompt kernel's, (format, dtype, block_tokens, key heads, query
+heads per key head, lengths, queries, tokens cut).  Many query heads per key
+head make the rows that it needs out of few queries.
+"""
 
 LONG = [1100, 40, 0, 700]          # more than 32 tiles of 32 tokens
 MANY = [int(x) for x in range(0, 36 * 26, 26)]      # 36 requests of at most 32 tiles
@@ -29,6 +36,17 @@ def cases():
         out.append(("alone odd", "int4", dtype, 16, 3, 4, [1100] * 2 + LONG, [1] * 6, True, (1, 1, 1, True)))
         out.append(("alone short", "int4", dtype, 64, 2, 8, [300, 64], [1, 1], False, (1, 1, 1, False)))
     return out
+
+
+PROMPTS = [
+    ("int4", "bf16", 64, 1, 128, [1100, 300], [37, 20], True),
+    ("int4", "f16", 16, 2, 75, [200], [64], False),
+    ("int4", "f32", 64, 1, 96, [130], [50], False),
+    ("fp8", "bf16", 7, 1, 128, [90, 60, 77], [38, 0, 40], False),
+    ("fp8", "f16", 64, 1, 64, [1300], [75], True),
+    ("fp8", "f32", 32, 2, 128, [600], [37], False),
+    ("int4", "bf16", 16, 4, 160, [150, 64, 100], [30, 20, 30], False),
+]
 
 
 def blocks_of(lens, tb):

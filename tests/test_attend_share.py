@@ -11,7 +11,7 @@ import subprocess
 import numpy as np
 import pytest
 
-from attend_paths import blocks_of, cases
+from attend_paths import PROMPTS, blocks_of, cases
 from conftest import ROOT
 
 FMT = {"fp8": 0, "int4": 1}
@@ -57,6 +57,11 @@ def test_cases_reach_their_paths(shares):
     for c, s in zip(cases(), shares(rows), strict=True):
         got = (s["hp"], s["nt"], s["set_heads"], s["ranges"] > 0)
         assert s["splits"] == 0 and got == c[9], c
+
+    rows = [(FMT[fmt], moved, 64, tb, h, len(lens), blocks_of(lens, tb), max(asks), sum(asks), h * group, DT[dtype])
+            for fmt, dtype, tb, h, group, lens, asks, _ in PROMPTS for moved in (False, True)]
+    for c, s in zip([c for c in PROMPTS for _ in range(2)], shares(rows), strict=True):
+        assert s["splits"] > 0 and (s["splits"] > 1) == c[7], (c, s["splits"])
 
 
 def test_sizes_hold(shares):

@@ -44,7 +44,7 @@ def bound(rec, fmt, h, want, spread, reach, moved):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["int4", "fp8"])
-@pytest.mark.parametrize("n,h,group", [(1, 2, 4), (4, 2, 4), (7, 2, 4), (110, 1, 4)])
+@pytest.mark.parametrize("n,h,group", [(1, 2, 4), (4, 2, 4), (7, 2, 4), (110, 1, 4), (37, 1, 128)])
 @pytest.mark.parametrize("moved", [False, True])
 def test_fp16_results(fmt, n, h, group, moved):
     say("fp16 weights", fmt, n, h, group, moved)

@@ -34,7 +34,7 @@ def records(g, fmt, nb, tb, h):
 # two tiles of 16 rows, a pair of heads, more tokens than one workgroup takes,
 # a prompt, one whose tokens are cut
 SHAPES = [(1, 1, 4, 16, 8), (7, 2, 4, 32, 6), (1, 8, 4, 64, 200), (3, 8, 8, 64, 200), (2, 2, 8, 16, 90), (110, 1, 4, 16, 8),
-          (200, 1, 2, 64, 21)]
+          (200, 1, 2, 64, 21), (37, 1, 128, 16, 8), (37, 1, 128, 64, 21)]
 
 
 @pytest.mark.parametrize("fmt,dtype", [("int4", "bf16"), ("int4", "f16"), ("fp8", "f32"), ("fp8", "bf16")])

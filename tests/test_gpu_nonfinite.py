@@ -50,15 +50,15 @@ def compare(q, rec, fmt, tb, h, table, lens, q_start, finite, what, **kw):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "f16"])
-@pytest.mark.parametrize("n", [1, 7, 110])
+@pytest.mark.parametrize("n,group", [(1, 4), (7, 4), (110, 4), (37, 128)])
 @pytest.mark.parametrize("moved", [False, True])
 @pytest.mark.parametrize("what", ["inf", "nan"])
-def test_other_rows_keep_their_precision(dtype, n, moved, what):
+def test_other_rows_keep_their_precision(dtype, n, group, moved, what):
     """One element of a row infinite or NaN, beside rows of 1e-6, 1e-3 and 1e5
-    (4e4 in fp16): 440 rows of a key head, 28, and one query's 4 heads."""
-    say("nonfinite query", dtype, n, moved, what)
+    (4e4 in fp16): one query's 4 heads, 28 rows of a key head, 440, 4,736."""
+    say("nonfinite query", dtype, n, group, moved, what)
     g = np.random.default_rng(n)
-    fmt, tb, h, group, nb = "int4", 16, 1, 4, 8
+    fmt, tb, h, nb = "int4", 16, 1, 8
     rec = pool(g, fmt, nb, tb, h)
     table = g.permutation(nb).astype(np.int32)[None]
     size = np.asarray((1e-6, 1e-3, 4e4 if dtype == "f16" else 1e5))[g.integers(0, 3, (n, group))]
@@ -77,7 +77,7 @@ def test_other_rows_keep_their_precision(dtype, n, moved, what):
 
 @pytest.mark.parametrize("fmt", ["int4", "fp8"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("n,h,group", [(110, 1, 4), (9, 2, 4), (2, 8, 2)])
+@pytest.mark.parametrize("n,h,group", [(110, 1, 4), (9, 2, 4), (2, 8, 2), (37, 1, 128)])
 @pytest.mark.parametrize("tb", [64, 16, 7])
 def test_nan_of_appended_tokens(fmt, dtype, n, h, group, tb):
     """Appended keys and values with a NaN element: rows that may not see the

@@ -30,11 +30,11 @@ def test_rope_of_whole_quarters(base, pairs, dtype):
 
 
 @pytest.mark.parametrize("base", BASES)
-@pytest.mark.parametrize("n", [2, 110])
-def test_attend_moved_by_whole_quarters(base, n):
+@pytest.mark.parametrize("n,group", [(2, 4), (110, 4), (37, 128)])
+def test_attend_moved_by_whole_quarters(base, n, group):
     """Records of keys that live in pairs 1 and 2 alone, moved by 4 positions;
     few rows and a prompt's."""
-    say("attend quarters", base, n)
+    say("attend quarters", base, n, group)
     g = np.random.default_rng(3)
     tb, h = 16, 1
     rec = hkv.alloc_records(1, 3, "fp8", tb, h, device=DEV)[0]
@@ -42,7 +42,7 @@ def test_attend_moved_by_whole_quarters(base, n):
     x[0, :, :, [i for i in range(128) if i % 64 not in (1, 2)]] = 0
     k, v = (torch.from_numpy(a).to(DEV, torch.float32) for a in x)
     hkv.append_tokens(k, v, torch.arange(48, device=DEV), rec, "fp8", tb)
-    q = torch.from_numpy(g.standard_normal((n, 4, 128))).to(DEV, torch.float32)
+    q = torch.from_numpy(g.standard_normal((n, group, 128))).to(DEV, torch.float32)
     table = np.array([[2, 0, 1]], np.int32)
     for move in (4, -4, 12, 2):
         check_attend(q, rec, "fp8", tb, h, table, [45], [0, n], f"moved {move}", causal=False, rope_base=base,
