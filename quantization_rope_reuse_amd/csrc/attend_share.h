@@ -15,19 +15,31 @@ struct Share {
 };
 
 // How a call's work is shared out, from the sizes that the host knows.
-inline Share share_of(int fmt, bool moved, const Geometry& g, const hkv_requests& req, int32_t n_tokens,
-               int32_t n_q_heads, int dtype) {
+inline Share share_of(int fmt, bool moved, const Geometry& g, const hkv_requests& req,
+                      int32_t n_tokens, int32_t n_q_heads, int dtype) {
   Share s = {};
   const int64_t queries = req.max_queries < n_tokens ? req.max_queries : n_tokens;
   const int64_t rows = queries * (n_q_heads / g.n_heads);
   s.splits = 0;
-  if (rows > 384) {
-    // The prompt kernel makes operands of codes once for 256 rows, the rows
-    // kernel for 32; but its eight waves wait for each other every 64 tokens.
-    // Of 32 query and 8 key heads behind 8,192 tokens, rows against prompt
-    // kernel: 40 queries of 2 requests 52 against 63 us, 100 queries 56
-    // against 56, 300 (behind 4,096) 69 against 66, 1,000 over FP8 258 against
-    // 260, with moved keys 434 against 364, fp32 663 against 530.
+  // The prompt kernel makes operands of codes once for 256 rows, the rows
+  // kernel for 32; but its eight waves wait for each other every 64 tokens, and
+  // a workgroup works as long on one row as on 256.  Of 32 query and 8 key
+  // heads over INT4 in bf16, rows against prompt kernel in us: one request
+  // behind 8,192 tokens, 50 queries 45 against 52, 100 queries 58 against 57,
+  // 400 129 against 135, 1,000 289 against 265 (fp32 659 against 531); four
+  // requests of 100 137 against 139 (FP8 168 against 139); eight first prompts
+  // of 256 53 against 32, one 14 against 26: even where it is level from 400
+  // rows on, the prompt kernel wins where it fills the CUs.
+  // Where requests have fewer rows on average than one of its workgroups,
+  // most of its workgroups hold little: 31 decodes of up to 8,192 tokens beside
+  // a prompt of 100 queries 90 against 492, of 512 226 against 873, 128 decodes
+  // of up to 2,048 called with 128 for the most queries 176 against 536.  Up to
+  // where the join's workgroups, one for every row that a request might have,
+  // cost what that spares (2^19 some 120 us).
+  const bool sparse = static_cast<int64_t>(n_tokens) * (n_q_heads / g.n_heads) <
+                          static_cast<int64_t>(kPromptRows) * req.n_requests &&
+                      queries * n_q_heads * req.n_requests <= (1 << 19);
+  if (rows > 384 && !sparse) {
     // One workgroup per 256 rows and key head; their tokens are cut where
     // these are too few for the CUs.
     s.items = (rows + kPromptRows - 1) / kPromptRows;

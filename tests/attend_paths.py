@@ -35,6 +35,12 @@ def cases():
         out.append(("alone", "fp8", dtype, 64, 8, 5, LONG, [3, 1, 2, 3], False, (1, 1, 1, True)))
         out.append(("alone odd", "int4", dtype, 16, 3, 4, [1100] * 2 + LONG, [1] * 6, True, (1, 1, 1, True)))
         out.append(("alone short", "int4", dtype, 64, 2, 8, [300, 64], [1, 1], False, (1, 1, 1, False)))
+    # decodes beside a prompt: most requests have fewer rows than a workgroup of the prompt kernel
+    steps = [int(x) for x in range(3, 1203, 75)]
+    for fmt, dtype, tb, moved in (("int4", "bf16", 64, False), ("fp8", "f16", 16, True), ("int4", "f32", 7, False)):
+        share = (1, 1 if moved or dtype == "f32" else 2, 2 if fmt == "int4" else 1, True)
+        out.append(("step", fmt, dtype, tb, 2, 4, steps, [1] * 15 + [110], moved, share))
+        out.append(("step first", fmt, dtype, tb, 4, 2, steps, [1] * 8 + [230] + [1] * 7, moved, share))
     return out
 
 

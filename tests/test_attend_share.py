@@ -86,6 +86,7 @@ def test_sizes_hold(shares):
             assert s["rows"] == (s["splits"] * n * hq if s["splits"] > 1 else 0)
             assert s["splits"] <= 256
         else:
+            assert group_rows <= 384 or (n * (hq // h) < 256 * r and queries * hq * r <= 1 << 19)
             heads = s["set_heads"] * s["hp"]
             assert heads * s["head_sets"] == h and heads in (1, 2)
             item = 16 * s["nt"] // s["hp"]
