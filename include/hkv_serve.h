@@ -102,8 +102,8 @@ int hkv_plan_step(const hkv_step* step, hipStream_t stream);
  *   phi_i = positions[axis[i]][t] / rope_base^(2 freq[i] / 128),
  *   (a, b) -> (a cos phi - b sin phi, a sin phi + b cos phi);
  * pairs with axis[i] = -1 and pairs whose angle is 0 pass through unchanged.
- * phi and its reduction modulo pi/2 are computed in double (accurate for
- * |phi| < 2^31), cos and sin of the reduced argument and the rotation in
+ * phi and its reduction modulo pi/2 are computed in double (for
+ * |phi| < 2^31, off by about 2^-51 of phi), cos and sin of the reduced argument and the rotation in
  * fp32, and the result is rounded once to dtype. */
 typedef struct {
   int32_t n_axes;        /* 1..8 */
@@ -173,13 +173,17 @@ typedef struct {
  * a row that sees nothing gets out = 0 and lse = -infinity.  k_m and v_m are
  * code * scale, taken into the products exactly: codes enter the matrix
  * instructions as they are and scales multiply scores and weights in fp32.
- * Sums are fp32.  Queries enter as fp16 where that is exact, else (fp32, or
- * turned by a shift) as two fp16 parts, 22 bits; weights as one fp16 part for
- * bf16 results, as two for the others.
+ * Sums are fp32.  Queries enter scaled by a power of two: as two fp16 parts
+ * (22 bits) where they are fp32 or turned by a shift, else as one, exact but
+ * for elements far below their row's largest, which are off by at most 2^-38
+ * of it (2^-24 in prompts, where rows of up to 2^14 in size share the power).
+ * Weights enter as one fp16 part (11 bits) for bf16 results, as two for the
+ * others.
  * What a token holds does not matter where its table entry is out of range or
- * where it stands past the end; a token that a row merely may not see yet must
- * not hold a NaN code (hkv_quant_* and hkv_append_tokens write none for
- * finite values).
+ * where it stands past the end.  FP8 records must not hold NaN codes (0x7F,
+ * 0xFF) elsewhere: rows that may not see the token yet, and another head's,
+ * could become NaN with it.  hkv_quant_* and hkv_append_tokens write none: of a
+ * vector with a NaN they make the scale NaN, which reaches what sees it alone.
  * q and out: dtype, n_tokens rows, the same number of heads, a multiple of
  * n_kv_heads; out must not overlap q.  lse: float [n_tokens][n_heads], or
  * NULL.  Rows of no request keep what out and lse held.

@@ -16,10 +16,11 @@ inline double quarter_turns(double rope_base, int freq) {
 
 // cos and sin of pos * theta, theta in quarter turns.  The product's whole
 // part k and remainder pos * theta - k (one fused step) are taken in double,
-// so the remainder is off by the rounding of theta alone, pos * theta *
-// 2^-53 quarter turns; the Taylor series of sin (to x^9) and cos (to x^10)
-// on |x| <= pi/4 leave out less than 2e-9 and 2e-11 and run in fp32, within
-// about one step of the exact values.  k < 2^31 for |pos * theta| < 2^31.
+// so the remainder is off by what theta is (a constant, a power and their
+// quotient, each rounded): some 2^-51 of the angle.  The Taylor series of sin
+// (to x^9) and cos (to x^10) on |x| <= pi/4 leave out less than 2e-9 and 2e-11
+// and run in fp32, within about one step of the exact values.  k < 2^31 for
+// |pos * theta| < 2^31.
 __device__ __forceinline__ void cos_sin(int pos, double theta, float* c, float* s) {
   const double p = static_cast<double>(pos);
   const double k = rint(p * theta);

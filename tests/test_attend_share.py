@@ -62,6 +62,10 @@ def test_cases_reach_their_paths(shares):
             for fmt, dtype, tb, h, group, lens, asks, _ in PROMPTS for moved in (False, True)]
     for c, s in zip([c for c in PROMPTS for _ in range(2)], shares(rows), strict=True):
         assert s["splits"] > 0 and (s["splits"] > 1) == c[7], (c, s["splits"])
+    # the paired heads of test_gpu_nonfinite.py
+    for s in shares([(fmt, moved, 4, tb, 8, 1, -(-4200 // tb), 2, 2, 32, dt) for fmt in (0, 1) for moved in (0, 1)
+                     for tb in (64, 16, 7) for dt in (0, 1, 2)]):
+        assert s["splits"] == 0 and s["hp"] == 2
 
 
 def test_sizes_hold(shares):

@@ -77,18 +77,20 @@ def test_other_rows_keep_their_precision(dtype, n, group, moved, what):
 
 @pytest.mark.parametrize("fmt", ["int4", "fp8"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("n,h,group", [(110, 1, 4), (9, 2, 4), (2, 8, 2), (37, 1, 128)])
+@pytest.mark.parametrize("n,h,group,room", [(110, 1, 4, 150), (9, 2, 4, 150), (2, 8, 2, 150), (37, 1, 128, 150),
+                                            (2, 8, 4, 4200)])       # the last: two heads share a score tile
 @pytest.mark.parametrize("tb", [64, 16, 7])
-def test_nan_of_appended_tokens(fmt, dtype, n, h, group, tb):
+def test_nan_of_appended_tokens(fmt, dtype, n, h, group, room, tb):
     """Appended keys and values with a NaN element: rows that may not see the
     token yet and other heads are as without it, the rest are NaN."""
-    say("nan appended", fmt, dtype, n, h, group, tb)
+    say("nan appended", fmt, dtype, n, h, group, room, tb)
     g = np.random.default_rng([n, h, tb])
     length = 150
     nb = -(-length // tb) + 1
     rec = hkv.alloc_records(1, nb, fmt, tb, h, device=DEV)[0]
     rec.zero_()
-    table = g.permutation(nb).astype(np.int32)[None]
+    table = np.full((1, max(-(-room // tb), nb)), -1, np.int32)
+    table[0, :nb] = g.permutation(nb)
     slots = table[0, np.arange(length) // tb].astype(np.int64) * tb + np.arange(length) % tb
     kv = g.standard_normal((2, length, h, 128))
     at_k, at_v = length - n // 2 - 1, length - 1
@@ -96,6 +98,8 @@ def test_nan_of_appended_tokens(fmt, dtype, n, h, group, tb):
     kv[1, at_v, h - 1, 100] = np.nan
     k, v = (torch.from_numpy(a).to(DEV, TORCH_OF[dtype]) for a in kv)
     hkv.append_tokens(k, v, dev(slots), rec, fmt, tb)
+    if fmt == "fp8":                     # NaN shows in the scales alone
+        assert not ((rec[:, :2 * tb * h * 128] & 127) == 127).any()
     q = torch.from_numpy(g.standard_normal((n, h * group, 128))).to(DEV, TORCH_OF[dtype])
     _, _, want = compare(q, rec, fmt, tb, h, table, [length], [0, n], None, "causal")
     bad = np.isnan(want).any(-1)
