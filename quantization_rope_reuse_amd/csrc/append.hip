@@ -4,8 +4,9 @@
 // The quantizer of the put (quant_device.h), 8 lanes per vector; a vector is
 // one (token, head) of K or V and finds its own record through its token's
 // slot.  It reads a vector and writes its codes and scale, so bytes bound it:
-// 32,777 tokens of 8 heads, fp16 to INT4, take 36 us, 4.7 TB/s of the 5.1 that
-// a copy reaches; 96 tokens, one launch's latency, 3 us.
+// 32,777 tokens of 8 heads, fp16 to INT4, take 37 us, 4.6 TB/s of the 6.2 that
+// a large elementwise pass reaches (from call to call 40, 4.2 TB/s; to FP8 43,
+// 4.8; from fp32 60 and 64, 5.1 and 5.3); 96 tokens, one launch's latency, 3.
 #include "quant_device.h"
 #include "serve_launch.h"
 

@@ -22,8 +22,9 @@
 //
 // Waves 0..3 bring the tiles to come after their work on a tile, waves 4..7, on
 // the same SIMDs, before it.  2,048 queries of 32 heads behind 16,384 tokens
-// (8 key heads, INT4) take 0.99 to 1.1 ms, 470 to 520 TFLOP/s of the 1,200
-// that a large library product reaches here.  Of a tile's 7,200 clocks a wave
+// (8 key heads, INT4) take 0.96 to 1.1 ms, 470 to 540 TFLOP/s of the 1,280
+// that a large library product reaches here (FP8 0.94; fp16 1.16 and fp32 2.0,
+// with two parts; moved keys 1.5).  Of a tile's 7,200 clocks a wave
 // spends 2 x 600 on scores, 2 x 1,000 on weights, 2 x 600 on the output, 1,100
 // on bringing; two waves per SIMD overlap little of that, and a third does not
 // fit the registers.  Products and weights interleaved in one instruction

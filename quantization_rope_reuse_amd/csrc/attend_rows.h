@@ -18,7 +18,10 @@
 // conversion.  Queries are scaled by a power of two per row into fp16's range
 // and split into two fp16 parts where one does not hold them (fp32 queries,
 // queries turned by -delta); weights likewise for fp32 and fp16 queries, whose
-// results an 11-bit weight would show in.  (bf16 results have 8 bits.)
+// results an 11-bit weight would show in.  (bf16 results have 8 bits: a second
+// part would bring their error against 64 bits from 0.00167 to 0.00165 of their
+// size, of moved keys from 0.00173 to 0.00171, and costs 1 to 4 % here, 15 % in
+// the prompt kernel.)
 //
 // Softmax: weights w = 2^14 exp2(s - m) v_scale enter their product as fp16, so
 // m is a reference (a whole number) that keeps both w (fp16) and the sum's
@@ -39,8 +42,8 @@
 // works on one.
 //
 // What bounds it: 32 requests of up to 8,192 tokens (64 query heads over 8,
-// INT4) take 43 to 47 us for 156 MB, 3.5 TB/s, and 6 us to join.  A lone
-// tile of two heads is some 450 vector instructions of 5 clocks (320 of them
+// INT4) take 43 to 47 us for 156 MB, 3.5 TB/s of the 6.2 that a large stream
+// reaches, and 6 us to join.  A lone tile of two heads is some 450 vector instructions of 5 clocks (320 of them
 // turn codes into fp16) beside 32 matrix instructions of 16; the waves' loops
 // run at the rate of memory, but setting out (requests, queries, first codes:
 // 13,000 of 90,000 clocks) and the join's waiting do not.  Wider layouts were
@@ -204,9 +207,10 @@ __device__ __forceinline__ void merge_rows(RowState<NT>& a, const f32x4* o, cons
   }
 }
 
-// QP, PP: fp16 parts of a query and of a weight (two for fp32).  TM: how block_tokens and
-// the tile of 32 tokens fit: kWhole, a tile lies in one block; kEighths,
-// runs of 8 tokens do; kAny.
+// QP, PP: fp16 parts of a query (two for fp32 and for moved keys) and of a
+// weight (two for fp32 and fp16).  TM: how block_tokens and the tile of 32
+// tokens fit: kWhole, a tile lies in one block; kEighths, runs of 8 tokens do;
+// kAny.
 enum TileMode { kWhole = 0, kEighths = 1, kAny = 2 };
 
 template <int FMT, int DT, int HP, int NT, int QP, int TM>
@@ -948,7 +952,7 @@ template <int FMT, int DT>
 hipError_t launch_rows_dtype(const AttendParams& p, int hp, int nt, dim3 grid, size_t bytes,
                              hipStream_t stream) {
   // two parts per query: 32 rows of them leave the registers, and 16 rows
-  // twice over are faster (58 against 132 us for drafts of five tokens of 16
+  // twice over are faster (54 against 145 us for drafts of five tokens of 16
   // requests over FP8 records)
   auto two_parts = [&] {
     return hp == 2 ? launch_rows_tiles<FMT, DT, 2, 1, 2>(p, grid, bytes, stream)

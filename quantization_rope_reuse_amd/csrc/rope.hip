@@ -9,7 +9,8 @@
 // which is also the gradient, changes the sine's sign.
 //
 // Bytes bound it: every element is read once and written once (40 heads of
-// 24,571 tokens in fp16: 89 us, 5.7 TB/s; a copy of the same size reaches 5.1).
+// 24,571 tokens in fp16: 84 us, 6.0 TB/s of the 6.2 that a large elementwise
+// pass reaches; torch's copy 5.1).
 // Stores pass the caches by (non-temporal), 4 % faster on large calls than
 // plain ones; one vector a lane group is as fast as two, three or five.
 #include "rope_device.h"

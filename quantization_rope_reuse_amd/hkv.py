@@ -868,7 +868,8 @@ def attend_records(q, records, fmt, block_tokens: int, n_kv_heads: int, block_ta
     block_table int32 [n_requests, max_blocks], kv_len int32 [n_requests] with
     the step's own tokens counted, q_start int32 [n_requests + 1] (None: one
     query per request), max_queries the most queries of a request (default
-    n_tokens; a smaller true bound saves empty work).  sm_scale: 1 / sqrt(128)
+    n_tokens; a smaller true bound saves workgroups and may choose a faster
+    kernel).  sm_scale: 1 / sqrt(128)
     if None.  causal: query j of n sees tokens up to kv_len - n + j.  delta_m:
     int32 [n_requests, max_blocks], moves the stored keys of each table entry
     as fetch_dequant_rope_shift does (rope_base, pairs).  workspace: True
