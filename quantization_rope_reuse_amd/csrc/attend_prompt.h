@@ -489,8 +489,9 @@ void attend_prompt_kernel(AttendParams p) {
           }
           // Where a row's weights outgrow fp16, its reference moves: by a power of
           // two while they are finite, found anew where they are not (or where
-          // the row does not see them all).
-          const bool anew = __any(!(big < INFINITY) || sum > 0x1p110f);
+          // the row does not see them all), or where weights of tokens without
+          // values grow: 2^26 times 2^100 is the most that l then holds.
+          const bool anew = __any(!(big < INFINITY) || sum > 0x1p100f);
           if (!anew && __any(big > 61440.0f)) {
             const float most_w = fmaxf(big, __shfl_xor(big, 32));
             const float up = most_w > 61440.0f ? rintf(__builtin_amdgcn_logf(most_w)) - 13.0f : 0.0f;

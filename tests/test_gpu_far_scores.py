@@ -74,3 +74,30 @@ def test_far_scores(fmt, dtype, shape):
         want = np.moveaxis(v, 0, 1)[np.arange(h)[None, :, None], s.argmax(-1)]
         ok = np.abs(got - want) <= np.abs(want) * eps + TINY[dtype]
         assert ok[alone].all(), f"{what}: {(~ok[alone]).any(-1).sum()} of {alone.sum()} rows"
+
+
+def test_sum_of_weights_of_zero_values():
+    """2^25 tokens whose values are zero, all but the first 64 of them 12 bits
+    above those in score: nothing of the result moves the reference, and the
+    sum of the weights has to stay finite.  One workgroup adds up 2^20 terms in
+    a lane, each sum rounded: lse is off by 2^20 * 2^-24 (and its own 2^-18)."""
+    say("zero values")
+    tb, group, n, r = 64, 128, 64, 8
+    rec = hkv.alloc_records(1, 2, "int4", tb, 1, device=DEV)[0]
+    k, v = torch.zeros(2, 2 * tb, 1, 128, device=DEV)
+    k[tb:, 0, 0] = 7.0
+    hkv.append_tokens(k, v, torch.arange(2 * tb, device=DEV), rec, "int4", tb)
+    blocks = 2 ** 25 // tb
+    table = torch.ones(r, blocks, dtype=torch.int32, device=DEV)
+    table[:, 0] = 0
+    q = torch.zeros(r * n, group, 128, device=DEV, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    scale = 12 * np.log(2) / 7
+    out, lse = hkv.attend_records(q, rec, "int4", tb, 1, table, torch.full((r,), 2 ** 25, dtype=torch.int32, device=DEV),
+                                  torch.arange(r + 1, dtype=torch.int32, device=DEV) * n, max_queries=n, causal=False,
+                                  sm_scale=scale)
+    torch.cuda.synchronize()
+    assert (out == 0).all()
+    want = np.log(64 + (2.0 ** 25 - 64) * 2.0 ** 12)
+    assert torch.isfinite(lse).all()
+    assert float((lse.double() - want).abs().max()) <= 2.0 ** -4 + 2.0 ** -18
