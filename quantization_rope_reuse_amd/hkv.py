@@ -865,6 +865,8 @@ def attend_records(q, records, fmt, block_tokens: int, n_kv_heads: int, block_ta
                    lse=None, workspace=True, stream=None):
     """Attention of q [n_tokens, n_q_heads, 128] over one layer's records
     [n_blocks, bytes]; returns (out, lse), lse float32 [n_tokens, n_q_heads].
+    Rows that belong to no request (padding) are not written: a tensor that the
+    call makes is not initialised there.
     block_table int32 [n_requests, max_blocks], kv_len int32 [n_requests] with
     the step's own tokens counted, q_start int32 [n_requests + 1] (None: one
     query per request), max_queries the most queries of a request (default

@@ -9,6 +9,7 @@ import torch
 
 from attend_paths import blocks_of, cases, name_of
 from parity_util import TORCH_OF
+from quantization_rope_reuse_amd import hkv
 from test_gpu_serve import DEV, check_attend, pool, say
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +36,23 @@ def test_path(case):
         kw = dict(delta_m=dm, rope_base=1e4, pairs="interleaved" if tb == 16 else "half_split")
     check_attend(q, rec, fmt, tb, h, table, lens, np.concatenate([[0], np.cumsum(asks)]), name_of(case),
                  max_queries=max(asks), **kw)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "fp8"])
+@pytest.mark.parametrize("tb", [64, 16, 7])
+def test_records_beyond_32_bits(fmt, tb):
+    """Records 600 MB apart, the last from byte 4.8e9 on; few rows, a pair of
+    heads, a prompt's rows."""
+    say("far records", fmt, tb)
+    g = np.random.default_rng(tb)
+    h, nb, stride = 2, 9, 600 * 1024 * 1024
+    rb = hkv.record_bytes(fmt, tb, h)
+    rec = torch.empty((nb - 1) * stride + rb, dtype=torch.uint8, device=DEV).as_strided((nb, rb), (stride, 1))
+    x = torch.from_numpy(g.standard_normal((2, nb * tb, h, 128)).astype(np.float32)).to(DEV)
+    hkv.append_tokens(x[0], x[1], torch.arange(nb * tb, device=DEV), rec, fmt, tb)
+    for n, group, room in ((1, 4, nb), (2, 4, 20000 // tb), (35, 64, nb)):
+        table = np.full((1, room), -1, np.int32)
+        table[0, :nb] = np.arange(nb - 1, -1, -1)
+        q = torch.from_numpy(1.5 * g.standard_normal((n, h * group, 128))).to(DEV, torch.bfloat16)
+        for dm in (None, np.full(table.shape, 50, np.int32)):
+            check_attend(q, rec, fmt, tb, h, table, [nb * tb - 3], [0, n], f"{n} queries", max_queries=n, delta_m=dm)
