@@ -7,3 +7,4 @@ code with the HIP library.
 from .hkv_oracle import *  # noqa: F401,F403
 from . import hkv_oracle  # noqa: F401
 from . import serve_oracle  # noqa: F401
+from . import pages_oracle  # noqa: F401

@@ -27,7 +27,10 @@ SOURCES = ("api.hip", "quant.hip", "fetch.hip", "crc.hip", "order.hip", "streams
            "select.hip", "frames.hip", "probe.hip", "noalloc.hip",
            "staged.hip", "serve_api.hip", "plan.hip", "rope.hip", "append.hip", "attend.hip",
            "attend_rows_int4.hip", "attend_rows_fp8.hip",
-           "attend_prompt_int4.hip", "attend_prompt_fp8.hip")
+           "attend_prompt_int4.hip", "attend_prompt_fp8.hip", "pages_api.hip", "append_pages.hip",
+           "join.hip", "attend_pages.hip",
+           *(f"attend_pages_{kind}_{t}.hip" for kind in ("rows", "chunk")
+             for t in ("bf16", "f16", "f32")))
 ARCH = "gfx950"
 
 

@@ -240,6 +240,10 @@ int element_size(int32_t dtype) { return elem_size(dtype); }
 
 int shape_check(const hkv_shape* shape, Geometry* g) { return check_shape(shape, g); }
 
+int pages_check(const hkv_pages* p, int32_t dtype, const hkv_shape* shape, PageView* v) {
+  return check_pages(p, dtype, shape, v);
+}
+
 int records_check(const hkv_records* r, int32_t fmt, const hkv_shape* shape, RecordView* v) {
   return check_records(r, fmt, shape, v);
 }

@@ -1,0 +1,566 @@
+// Attention over pages, included by one source per element type.
+//
+// A key head's rows are its query heads times the request's queries.  A wave
+// takes 32 of them and walks the cached tokens in subtiles of 32 with the
+// matrix instruction 32x32 (16 inner steps in 16-bit types, 2 in fp32), fp32
+// sums, keys and values its first operand:
+//   scores  S^T = K Q^T    32 tokens x 32 rows
+//   output  O^T = V^T P^T  4 times 32 dims x 32 rows
+// so that a lane (q, h) = (lane % 32, lane / 32) holds scores of one row,
+// tokens 8a + 4h + b in register 4a + b, which are the weights it has to supply
+// to the second product (whose inner order is free): no exchange of lanes.
+//
+// Tiles lie in LDS as they lie in the pages, a token's 128 dims a row; tokens
+// that do not exist are read from a place of zeros.  Rows are cut in chunks of
+// 16 bytes whose place is XORed with the token, so that lanes reading the same
+// chunk of several tokens meet different banks.  Values reach the operand,
+// which wants several tokens of one dim, through gfx950's transposing LDS read.
+//
+// Softmax: weights w = exp2(s - m + kOff) with a whole reference m per row that
+// moves only when a tile's scores exceed it by kSlack, which spares most tiles
+// the rescaling of O and the reduction across lanes.  16-bit floats keep their
+// weights in the type's normal numbers down to 2^-(14 + kOff) of the reference
+// (fp16); bf16's and fp32's range needs no offset.
+//
+// A masked token's weight is 0, but 0 times an infinite value is not: where a
+// row's sum is finite and its output is not, it is computed again, token by
+// token, over what it sees (careful_row).
+#pragma once
+
+#include "attend_pages_launch.h"
+#include "hkv_device.h"
+
+namespace hkv {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
+
+constexpr int kSub = 32;                   // tokens of a subtile
+constexpr float kNoReference = -3.0e38f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kFar = 0x1p16f;            // references from here on: scores are rounded before m is taken off
+
+// Where tokens that do not exist are read.
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+template <int DT> struct PageTraits;
+template <> struct PageTraits<kBF16> {
+  static constexpr float kOff = 0.0f, kSlack = 8.0f;
+};
+template <> struct PageTraits<kF16> {
+  static constexpr float kOff = 12.0f, kSlack = 3.0f;
+};
+template <> struct PageTraits<kF32> {
+  static constexpr float kOff = 0.0f, kSlack = 8.0f;
+};
+
+// Geometry of a token's row in LDS.
+template <int DT>
+struct Row {
+  static constexpr int ES = ElemSize<DT>::value;
+  static constexpr int kBytes = kHeadDim * ES;
+  static constexpr int kChunks = kBytes / 16;       // lanes that bring one row
+  static constexpr int kPerWave = kWave / kChunks;  // rows of a wave's load
+  static __device__ __forceinline__ int key(int token, int chunk) { return chunk ^ (token & 15); }
+  static __device__ __forceinline__ int value(int token, int chunk) {
+    return DT == kF32 ? chunk ^ (2 * (token & 4)) : chunk ^ (4 * (token & 3));
+  }
+};
+
+struct PageSpan {        // a request's queries and cached tokens
+  int start, n_q, rows;  // rows: of a key head, of the queries that are computed
+  int len, pre;          // pre: tokens of the prefix
+};
+
+__device__ __forceinline__ PageSpan page_span(const PageAttendParams& p, int r) {
+  PageSpan s;
+  s.start = p.q_start ? min(max(p.q_start[r], 0), p.n_tokens) : r;
+  const int end = p.q_start ? min(max(p.q_start[r + 1], 0), p.n_tokens) : r + 1;
+  s.n_q = max(end - s.start, 0);
+  s.rows = min(s.n_q, p.max_queries) * p.group;
+  s.len = min(max(p.kv_len[r], 0), p.max_len);
+  s.pre = p.prefix ? min(max(p.prefix[r], 0), s.len) : 0;
+  return s;
+}
+
+struct Sight {           // tokens [0, pre) and [lo, hi), hi >= lo
+  int pre, lo, hi;
+  int pos;
+};
+
+// What row j of a request sees.
+__device__ __forceinline__ Sight sight_of(const PageAttendParams& p, const PageSpan& s, int j) {
+  Sight v;
+  const int query = s.start + j;
+  v.pos = p.positions ? p.positions[query] : s.len - s.n_q + j;
+  if (p.positions && v.pos < 0) return {0, 0, 0, v.pos};
+  const int at = max(v.pos, -1);
+  v.pre = s.pre;
+  v.hi = p.causal ? min(at, s.len - 1) + 1 : s.len;
+  v.lo = p.begin ? max(p.begin[query], 0) : 0;
+  if (p.window > 0) v.lo = max(v.lo, at - p.window + 1);
+  v.lo = min(v.lo, v.hi);
+  return v;
+}
+
+__device__ __forceinline__ int wave_min(int x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = min(x, __shfl_xor(x, off));
+  return __builtin_amdgcn_readfirstlane(x);
+}
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = max(x, __shfl_xor(x, off));
+  return __builtin_amdgcn_readfirstlane(x);
+}
+
+// What a set of rows sees: bounds for whole tiles.
+struct View {
+  int pre_least, pre_most, lo_least, lo_most, hi_least, hi_most;
+  // every row sees all of [a, a + n)
+  __device__ __forceinline__ bool all(int a, int n) const {
+    return (a >= lo_most && hi_least - a >= n) || pre_least - a >= n;
+  }
+  // some row may see some of [a, a + n)
+  __device__ __forceinline__ bool some(int a, int n) const {
+    return a < pre_most || (a < hi_most && lo_least - a < n);
+  }
+};
+
+__device__ __forceinline__ View view_of_wave(const Sight& v) {
+  // (rows that see nothing beyond the prefix do not widen the range)
+  const bool any = v.hi > v.lo;
+  return {wave_min(v.pre), wave_max(v.pre), wave_min(any ? v.lo : INT32_MAX), wave_max(any ? v.lo : INT32_MAX),
+          wave_min(any ? v.hi : 0), wave_max(any ? v.hi : 0)};
+}
+
+// Tiles of `size` tokens that a view has: [0, pre) and [lo, hi).
+struct TileList {
+  int pre, lo, count;
+  __device__ __forceinline__ int at(int i) const { return i < pre ? i : i - pre + lo; }
+};
+
+__device__ __forceinline__ TileList tiles_of_view(int pre, int lo, int hi, int size) {
+  TileList t;
+  t.pre = (pre + size - 1) / size;
+  const int end = hi / size + (hi % size != 0);
+  t.lo = max(min(lo, hi) / size, t.pre);
+  t.count = t.pre + max(end - t.lo, 0);
+  return t;
+}
+
+// The quotient of a token and block_tokens.
+__device__ __forceinline__ int block_of(const PageAttendParams& p, int token) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(token)) * p.block_magic) >> p.block_shift);
+}
+
+// A row of queries as operands.  keep and flip: masks of their bits, which turn
+// the sign over where sm_scale is negative and make them 0 where it is 0, so
+// that the scale itself is positive.
+template <int DT>
+struct Queries {
+  s8 x[8];
+  __device__ __forceinline__ void load(const char* row, int h, uint32_t keep, uint32_t flip) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      u32x4 raw = *reinterpret_cast<const u32x4*>(row + (16 * kk + 8 * h) * 2);
+      raw = (raw & keep) ^ flip;
+      x[kk] = __builtin_bit_cast(s8, raw);
+    }
+  }
+};
+template <>
+struct Queries<kF32> {
+  f32x4 x[16];
+  __device__ __forceinline__ void load(const char* row, int h, uint32_t keep, uint32_t flip) {
+#pragma unroll
+    for (int kk = 0; kk < 16; ++kk) {
+      u32x4 raw = *reinterpret_cast<const u32x4*>(row + (64 * h + 4 * kk) * 4);
+      raw = (raw & keep) ^ flip;
+      x[kk] = __builtin_bit_cast(f32x4, raw);
+    }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ f32x16 mma(s8 a, s8 b, f32x16 c) {
+  if constexpr (DT == kBF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+
+// A copy of x that the compiler takes for a new value: what is computed from
+// it stays where it stands instead of holding registers across a loop.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// S^T of the subtile's 32 tokens (rows of `keys`, the first a multiple of 32).
+template <int DT>
+__device__ __forceinline__ f32x16 score_tile(const char* keys, const Queries<DT>& q, int lane) {
+  const int id = here(lane);
+  const int token = id & 31, h = id >> 5;
+  // (a step moves the chunk's place by bits of its own: rows are aligned)
+  const int at = token * Row<DT>::kBytes + (Row<DT>::key(token, DT == kF32 ? 16 * h : h) << 4);
+  f32x16 acc = {};
+  if constexpr (DT == kF32) {
+#pragma unroll
+    for (int kk = 0; kk < 16; ++kk) {
+      const f32x4 k = *reinterpret_cast<const f32x4*>(keys + (at ^ (kk << 4)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(k[i], q.x[kk][i], acc, 0, 0, 0);
+    }
+  } else {
+    // all reads first, so that the products wait once
+    s8 k[8];
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) k[kk] = *reinterpret_cast<const s8*>(keys + (at ^ (kk << 5)));
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) acc = mma<DT>(k[kk], q.x[kk], acc);
+  }
+  return acc;
+}
+
+// 8 weights as an operand, and (PP = 2) what rounding them left out.
+template <int DT, int PP>
+struct Weights {
+  s8 part[PP][2];
+  __device__ __forceinline__ void set(const float (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (DT == kBF16) {
+        const __bf16 hi = static_cast<__bf16>(w[i]);
+        part[0][i >> 3][i & 7] = __builtin_bit_cast(short, hi);
+        if constexpr (PP > 1)
+          part[1][i >> 3][i & 7] = __builtin_bit_cast(short, static_cast<__bf16>(w[i] - static_cast<float>(hi)));
+      } else {
+        const _Float16 hi = static_cast<_Float16>(w[i]);
+        part[0][i >> 3][i & 7] = __builtin_bit_cast(short, hi);
+        if constexpr (PP > 1)
+          part[1][i >> 3][i & 7] = __builtin_bit_cast(short, static_cast<_Float16>(w[i] - static_cast<float>(hi)));
+      }
+    }
+  }
+};
+template <int PP>
+struct Weights<kF32, PP> {
+  float w[16];
+  __device__ __forceinline__ void set(const float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = x[i];
+  }
+};
+
+typedef __attribute__((address_space(3))) s4* LdsS4;
+
+// O^T += V^T P^T over the subtile's 32 tokens.
+template <int DT, int PP>
+__device__ __forceinline__ void output_tile(const char* values, const Weights<DT, PP>& w, f32x16 (&o)[4],
+                                            int lane) {
+  const int id = here(lane);
+  const int h = id >> 5;
+  if constexpr (DT == kF32) {
+    const int dim = id & 31;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int token = 8 * (i >> 2) + 4 * h + (i & 3);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int chunk = 8 * d + (dim >> 2);
+        const float v = *reinterpret_cast<const float*>(values + token * Row<DT>::kBytes +
+                                                        (Row<DT>::value(token, chunk) << 4) + 4 * (dim & 3));
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, w.w[i], o[d], 0, 0, 0);
+      }
+    }
+  } else {
+    // A read takes 4 tokens of 16 dims for 16 lanes, lane i supplying the
+    // address of token i / 4, dims 4 (i % 4) .., and getting dim i.
+    const int i = id & 15;
+    const int token = 4 * h + (i >> 2);
+    // (d moves the chunk's place by bits of its own)
+    const int base = token * Row<DT>::kBytes + (Row<DT>::value(token, 2 * ((id >> 4) & 1) + ((i >> 1) & 1)) << 4) + 8 * (i & 1);
+    s8 v[2][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const char* at = values + (base ^ (d << 6)) + 16 * s * Row<DT>::kBytes;
+        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)(at));
+        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)(at + 8 * Row<DT>::kBytes));
+        v[s][d] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int pp = PP - 1; pp >= 0; --pp)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] = mma<DT>(v[s][d], w.part[pp][s], o[d]);
+  }
+}
+
+// How scores become exponents of two.  Without cap and bias the product is
+// scaled in the step that takes the reference off.
+struct ScoreScale {
+  float scale;       // sm_scale log2(e), or (CAP) sm_scale / cap; positive
+  float top;         // (CAP) cap log2(e)
+  float slope;       // (BIAS) the head's, times log2(e)
+};
+
+// tanh(y): the fraction of exponentials, which loses bits beside 0, or the
+// first terms of the series, which leave out less than 2^-21 of it there.
+__device__ __forceinline__ float tanh_of(float y) {
+  const float a = fabsf(y), y2 = y * y;
+  const float e = __builtin_amdgcn_exp2f(-2.88539008177792681472f * a);
+  const float big = (1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e);
+  float c = __builtin_fmaf(y2, -17.0f / 315.0f, 2.0f / 15.0f);
+  c = __builtin_fmaf(c, y2, -1.0f / 3.0f);
+  const float small = __builtin_fmaf(y * y2, c, y);
+  return a < 0.25f ? small : __builtin_copysignf(big, y);
+}
+
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score_of(float x, const ScoreScale& f, float distance) {
+#pragma clang fp contract(off)
+  float s = x * f.scale;
+  if constexpr (CAP) s = tanh_of(s) * f.top;
+  if constexpr (BIAS) s = s - f.slope * distance;
+  return s;
+}
+
+// State of a wave's rows.
+struct RowsState {
+  f32x16 o[4];
+  float m, l;        // the reference; this lane's part of the sum
+  bool far;          // some row's reference is
+};
+
+// Bits of the tokens that a row sees of a tile of up to 64 from `first` on, of
+// which `live` exist, bit 0 that of register 0.
+__device__ __forceinline__ uint64_t seen_of(const Sight& v, uint64_t live, int first, int h) {
+  auto below = [&](int end) {            // tokens before `end`
+    const int n = min(max(end - first, 0), 64);
+    return n == 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
+  };
+  return (live & (below(v.pre) | (below(v.hi) & ~below(v.lo)))) >> (4 * h);
+}
+
+// The weights of a tile of N subtiles from its products.  part: some row may
+// not see all of it; seen: what the lane's row sees of it (seen_of); from_first:
+// the row's position, counted from the token of register 0.
+template <int DT, int PP, bool CAP, bool BIAS, int N>
+__device__ __forceinline__ void weigh_tile(f32x16 (&acc)[N], Weights<DT, PP> (&out)[N], RowsState& st,
+                                           const ScoreScale& f, float from_first, bool part, uint64_t seen) {
+  constexpr float kOff = PageTraits<DT>::kOff, kSlack = PageTraits<DT>::kSlack;
+  constexpr bool kPlain = !CAP && !BIAS;
+  if constexpr (!kPlain) {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        acc[u][i] = score_of<CAP, BIAS>(acc[u][i], f, fabsf(from_first - (kSub * u + 8 * (i >> 2) + (i & 3))));
+  }
+  if (part) {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[u][i] = (seen >> (kSub * u + 8 * (i >> 2) + (i & 3))) & 1 ? acc[u][i] : -INFINITY;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, acc[u][i]);
+  if constexpr (kPlain) top *= f.scale;            // (scale > 0)
+  if (__any(top > st.m + kSlack)) {
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m = top > st.m + kSlack ? ceilf(top) : st.m;
+    const float keep = m == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+    st.m = m;
+    st.l *= keep;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) st.o[d] *= keep;
+    st.far = __any(fabsf(m) >= kFar && m != kNoReference);
+  }
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    float w[16];
+    if (!kPlain || st.far) {
+      // the reference came from rounded scores: so do the weights
+#pragma clang fp contract(off)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float s = kPlain ? acc[u][i] * f.scale : acc[u][i];
+        w[i] = (s - st.m) + kOff;
+      }
+    } else {
+      const float shift = kOff - st.m;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = __builtin_fmaf(acc[u][i], f.scale, shift);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      w[i] = __builtin_amdgcn_exp2f(w[i]);
+      sum += w[i];
+    }
+    st.l += sum;
+    out[u].set(w);
+  }
+}
+
+// 16 bytes per lane straight into LDS: lane i's to `to` + 16 i.
+__device__ __forceinline__ void bring16(const char* from, char* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(from),
+                                   (__attribute__((address_space(3))) uint32_t*)(to), 16, 0, 0);
+}
+
+// Waits until at most N of the wave's loads are under way (they arrive in
+// order), and for its LDS reads.  Nothing moves across.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "vmcnt has 6 bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
+}
+
+// log(2^m l), m a whole number; -infinity for l = 0.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  const int e = l > 0.0f && l < INFINITY ? __builtin_amdgcn_frexp_expf(l) : 0;
+  return (__builtin_amdgcn_logf(__builtin_ldexpf(l, -e)) + (m + static_cast<float>(e))) * kLn2;
+}
+
+// The tiles that a wave has worked on: first, first + step, .. of a list.
+struct WaveTiles {
+  TileList list;
+  int first, end, step, size;
+};
+
+// The output of one row over a wave's tiles, token by token, lane i dims 2i and
+// 2i + 1: sum_m exp2(s_m - m) v_m / l over the tokens it sees with a weight
+// above 0.
+template <int DT, bool CAP, bool BIAS>
+__device__ __forceinline__ float2 careful_row(const PageAttendParams& p, const int32_t* table,
+                                                        int64_t head_off, const char* q_row, Sight v, int len,
+                                                        WaveTiles w, float m, float l, ScoreScale f) {
+  constexpr int ES = ElemSize<DT>::value;
+  const int lane = threadIdx.x & (kWave - 1);
+  auto two = [&](const char* at, float (&x)[2]) {
+    if constexpr (DT == kF32) {
+      const float2 y = reinterpret_cast<const float2*>(at)[lane];
+      x[0] = y.x;
+      x[1] = y.y;
+    } else {
+      const uint32_t y = reinterpret_cast<const uint32_t*>(at)[lane];
+      x[0] = DT == kF16 ? f16_bits_to_f32(y & 0xFFFFu) : bf16_bits_to_f32(y & 0xFFFFu);
+      x[1] = DT == kF16 ? f16_bits_to_f32(y >> 16) : bf16_bits_to_f32(y >> 16);
+    }
+  };
+  static_assert(ES == 2 || ES == 4, "element sizes");
+  float q[2];
+  two(q_row, q);
+  const float sign = p.q_keep == 0 ? 0.0f : p.q_flip ? -1.0f : 1.0f;
+  float2 o = make_float2(0.0f, 0.0f);
+  for (int i = w.first; i < w.end; i += w.step) {
+    const int first = w.list.at(i) * w.size;
+    const int last = min(w.size, len - first);
+    for (int t = 0; t < last; ++t) {
+      const int token = first + t;
+      if (token >= v.pre && (token < v.lo || token >= v.hi)) continue;
+      const int block = block_of(p, token);
+      const int entry = table[block];
+      if (static_cast<uint32_t>(entry) >= static_cast<uint32_t>(p.num_pages)) continue;
+      const int64_t at = entry * p.page + (token - block * p.block_tokens) * p.token + head_off;
+      float k[2], x[2];
+      two(p.k + at, k);
+      float s = (q[0] * k[0] + q[1] * k[1]) * sign;
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+      const float distance = fabsf(static_cast<float>(static_cast<double>(v.pos) - token));
+      const float weight = __builtin_amdgcn_exp2f((score_of<CAP, BIAS>(s, f, distance) - m) + PageTraits<DT>::kOff) / l;
+      if (weight > 0.0f) {
+        two(p.v + at, x);
+        o.x += weight * x[0];
+        o.y += weight * x[1];
+      }
+    }
+  }
+  return o;
+}
+
+// Divides the sum out (l becomes the row's whole sum of this wave's tokens) and
+// computes again the rows that a masked token's value has spoilt.
+template <int DT, bool CAP, bool BIAS>
+__device__ __forceinline__ void finish_rows(const PageAttendParams& p, const int32_t* table, int64_t head_off,
+                                            const char* q_row, const Sight& v, int len, const WaveTiles& w,
+                                            RowsState& st, const ScoreScale& f, int lane) {
+  st.l += __shfl_xor(st.l, 32);
+  const float inv = 1.0f / st.l;
+  bool bad = false;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float y = st.l == 0.0f ? 0.0f : st.o[d][i] * inv;
+      st.o[d][i] = y;
+      bad = bad || !(fabsf(y) < INFINITY);
+    }
+  bad = bad && st.l < INFINITY;
+  uint64_t rows = __ballot(bad);
+  rows = (rows | (rows >> 32)) & 0xFFFFFFFFu;
+  while (rows) {
+    const int c = __builtin_ctzll(rows);
+    rows &= rows - 1;
+    const uint64_t at = reinterpret_cast<uint64_t>(q_row);
+    const uint64_t row = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(at >> 32), c)) << 32 |
+                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(at), c));
+    const Sight sight = {__builtin_amdgcn_readlane(v.pre, c), __builtin_amdgcn_readlane(v.lo, c),
+                         __builtin_amdgcn_readlane(v.hi, c), __builtin_amdgcn_readlane(v.pos, c)};
+    const ScoreScale g = {f.scale, f.top, __shfl(f.slope, c)};
+    const float2 y = careful_row<DT, CAP, BIAS>(p, table, head_off, reinterpret_cast<const char*>(row), sight, len, w,
+                                                __shfl(st.m, c), __shfl(st.l, c), g);
+    const int h = lane >> 5;
+    const bool mine = (lane & 31) == c;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        // dim 32 d + 8 (i / 4) + 4 h + i % 4
+        const float x = __shfl(i & 1 ? y.y : y.x, 16 * d + 4 * (i >> 2) + 2 * h + ((i & 3) >> 1));
+        st.o[d][i] = mine ? x : st.o[d][i];
+      }
+  }
+  st.l *= __builtin_amdgcn_exp2f(-PageTraits<DT>::kOff);
+}
+
+// 4 consecutive dims of a row.
+template <int DT>
+__device__ __forceinline__ void store4(char* p, const float (&x)[4]) {
+  if constexpr (DT == kF32) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+  } else {
+    u32x2 y;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = DT == kF16 ? f32_to_f16_bits(x[2 * i]) : f32_to_bf16_bits(x[2 * i]);
+      const uint32_t hi = DT == kF16 ? f32_to_f16_bits(x[2 * i + 1]) : f32_to_bf16_bits(x[2 * i + 1]);
+      y[i] = lo | (hi << 16);
+    }
+    *reinterpret_cast<u32x2*>(p) = y;
+  }
+}
+
+// The slope and scales of a head's rows.
+template <bool BIAS>
+__device__ __forceinline__ ScoreScale scale_of(const PageAttendParams& p, int head) {
+  return {p.scale, p.cap_log2, BIAS ? p.slopes[head] * 1.44269504088896340736f : 0.0f};
+}
+
+}  // namespace hkv

@@ -1,0 +1,10 @@
+// The chunk kernel of attention over pages in f16.
+#include "attend_pages_chunk.h"
+
+namespace hkv {
+
+hipError_t launch_page_chunk_f16(const PageAttendParams& p, dim3 grid, hipStream_t stream) {
+  return launch_page_chunk<kF16>(p, grid, stream);
+}
+
+}  // namespace hkv

@@ -14,6 +14,7 @@
 #include <string>
 
 #include "hkv.h"
+#include "hkv_pages.h"
 #include "hkv_serve.h"
 
 namespace {
@@ -31,6 +32,10 @@ struct Calls {
   decltype(&hkv_fetch_dequant_rope_shift) fetch = nullptr;
   decltype(&hkv_fetch_dequant_rope_shift_tokens) fetch_tokens = nullptr;
   decltype(&hkv_record_bytes) record_bytes = nullptr;
+  decltype(&hkv_append_pages) append_pages = nullptr;
+  decltype(&hkv_attend_pages) attend_pages = nullptr;
+  decltype(&hkv_attend_pages_workspace_bytes) attend_pages_bytes = nullptr;
+  decltype(&hkv_join_attention) join = nullptr;
 } calls;
 
 void bind(const py::dict& at) {
@@ -45,6 +50,10 @@ void bind(const py::dict& at) {
   set(calls.fetch, "hkv_fetch_dequant_rope_shift");
   set(calls.fetch_tokens, "hkv_fetch_dequant_rope_shift_tokens");
   set(calls.record_bytes, "hkv_record_bytes");
+  set(calls.append_pages, "hkv_append_pages");
+  set(calls.attend_pages, "hkv_attend_pages");
+  set(calls.attend_pages_bytes, "hkv_attend_pages_workspace_bytes");
+  set(calls.join, "hkv_join_attention");
 }
 
 // A library call, without the interpreter's lock: a launch waits where the
@@ -367,6 +376,146 @@ int fetch(bool per_token, const Tensor& records, int fmt, const Tensor& block_ta
                 &pages, dtype_of(k), stream_of(stream, on.device()).stream());
 }
 
+// One layer's pages, [P, T_b, H, 128] or [1, P, T_b, H, 128].
+struct PagePool {
+  hkv_shape shape;
+  hkv_pages pages;
+  int dtype;
+};
+PagePool page_pool_of(const Tensor& k_pages, const Tensor& v_pages) {
+  const Tensor k = as_5d(k_pages), v = as_5d(v_pages);
+  need(k.size(0) == 1, "pages must be one layer's [P, T_b, H, 128] tensors");
+  need(k.sizes() == v.sizes() && k.strides() == v.strides() && k.scalar_type() == v.scalar_type(),
+       "K and V pages must share shape, strides and dtype");
+  need(k.size(4) == HKV_HEAD_DIM && k.stride(4) == 1,
+       "the last (head_dim=128) axis of the pages must be contiguous");
+  if (dtype_of(k) < 0) refuse("unsupported page dtype " + dtype_name(k));
+  // the stride of an axis of one entry addresses nothing and may be anything
+  const auto stride = [&](int d) { return k.size(d) > 1 ? k.stride(d) : 0; };
+  return {{1, small(k.size(1), "num_pages"), small(k.size(2), "block_tokens"), small(k.size(3), "n_kv_heads"),
+           HKV_HEAD_DIM},
+          {k.data_ptr(), v.data_ptr(), 0, stride(1), stride(2), stride(3), small(k.size(1), "num_pages")},
+          dtype_of(k)};
+}
+
+// axes: address of an hkv_rope_axes, 0 for none.
+py::tuple append_pages(const Tensor& k, const Tensor& v, const Tensor& slots, const Tensor& k_pages,
+                       const Tensor& v_pages, const Maybe& positions, uintptr_t axes, const Maybe& q,
+                       const Maybe& q_out, const py::object& stream) {
+  OneGpu on("append_pages");
+  on(k)(v)(slots)(k_pages)(v_pages)(positions)(q)(q_out);
+  const auto at_stream = stream_of(stream, on.device());
+  const auto* a = reinterpret_cast<const hkv_rope_axes*>(axes);
+  const PagePool pool = page_pool_of(k_pages, v_pages);
+  const hkv_heads kh = heads_of(k, "k"), vh = heads_of(v, "v");
+  const int64_t n = k.size(0);
+  need(k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type(), "k and v must share shape and dtype");
+  need(slots.scalar_type() == at::kLong && slots.is_contiguous() && slots.numel() == n,
+       "slots must be a contiguous int64 tensor of n_tokens elements");
+  need((a != nullptr) == positions.has_value(), "positions and rope_base go together");
+  need(!q || a, "queries are only taken with positions");
+  int64_t rows = 1;
+  if (positions) {
+    rows = positions->dim() == 1 ? 1 : positions->size(0);
+    if ((positions->dim() != 1 && positions->dim() != 2) || positions->scalar_type() != at::kInt ||
+        rows != a->n_axes || positions->size(-1) != n || (n > 1 && positions->stride(-1) != 1))
+      refuse("positions must be int32 [" + std::to_string(a->n_axes) + ", n_tokens], last axis contiguous");
+  }
+  hkv_heads qh = {}, oh = {};
+  Maybe qo = q_out;
+  need(q || !q_out, "q_out needs q");
+  if (q) {
+    if (!qo) qo = made_on(q->sizes(), q->options(), at_stream);
+    qh = heads_of(*q, "q");
+    oh = heads_of(*qo, "q_out");
+    need(q->size(0) == n && q->scalar_type() == k.scalar_type() && qo->sizes() == q->sizes() &&
+             qo->scalar_type() == q->scalar_type(),
+         "q, k and v must share dtype and n_tokens, q_out q's shape");
+  }
+  const int st = launch(calls.append_pages, &pool.shape, a,
+                        positions ? static_cast<const int32_t*>(positions->data_ptr()) : nullptr,
+                        positions && rows > 1 ? positions->stride(0) : 0, &qh, &kh, &vh, &oh, dtype_of(k),
+                        small(n, "n_tokens"), static_cast<const int64_t*>(slots.data_ptr()), &pool.pages,
+                        pool.dtype, at_stream.stream());
+  return py::make_tuple(st, qo);
+}
+
+// workspace: True (made here where one is needed), None or a uint8 tensor.
+// max_queries: -1 for the default.
+py::tuple attend_pages(const Tensor& q, const Tensor& k_pages, const Tensor& v_pages, const Tensor& block_table,
+                       const Tensor& kv_len, const Maybe& q_start, int64_t max_queries, double sm_scale,
+                       bool causal, const Maybe& positions, const Maybe& begin, const Maybe& prefix_len,
+                       int64_t window, double cap, const Maybe& slopes, const Maybe& out_, const Maybe& lse_,
+                       const py::object& workspace, const py::object& stream) {
+  OneGpu on("attend_pages");
+  on(q)(k_pages)(v_pages)(block_table)(kv_len)(q_start)(positions)(begin)(prefix_len)(slopes)(out_)(lse_);
+  Maybe ws;
+  const bool make = workspace.is(py::bool_(true));
+  if (!make && !workspace.is_none()) ws = py::cast<Tensor>(workspace);
+  on(ws);
+  const auto at_stream = stream_of(stream, on.device());
+  const PagePool pool = page_pool_of(k_pages, v_pages);
+  const hkv_heads qh = heads_of(q, "q");
+  need(dtype_of(q) == pool.dtype, "q and the pages must share one dtype");
+  const int64_t n = q.size(0), hq = q.size(1);
+  const Table table = table_of(block_table);
+  const int64_t R = block_table.size(0);
+  need(kv_len.numel() == R && (q_start ? q_start->numel() == R + 1 : n == R),
+       "kv_len [n_requests], q_start [n_requests + 1] (or one query per request) and block_table must agree");
+  need((!positions || positions->numel() == n) && (!begin || begin->numel() == n) &&
+           (!prefix_len || prefix_len->numel() == R),
+       "positions and begin must hold n_tokens entries, prefix_len n_requests");
+  need(!slopes || (slopes->numel() == hq && slopes->scalar_type() == at::kFloat && slopes->is_contiguous()),
+       "slopes must be a contiguous float32 tensor of n_q_heads elements");
+  if (max_queries < 0) max_queries = q_start ? (n > 1 ? n : 1) : 1;
+  const Tensor out = out_ ? *out_ : made_on(q.sizes(), q.options(), at_stream);
+  need(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type(), "out must have q's shape and dtype");
+  const Tensor lse = lse_ ? *lse_ : made_on({n, hq}, q.options().dtype(at::kFloat), at_stream);
+  need(lse.dim() == 2 && lse.size(0) == n && lse.size(1) == hq && lse.scalar_type() == at::kFloat &&
+           lse.is_contiguous(),
+       "lse must be a contiguous float32 [n_tokens, n_q_heads] tensor");
+  const hkv_requests req = {small(R, "n_requests"), small(table.blocks, "max_blocks"),
+                            small(max_queries, "max_queries"), table.data, table.stride,
+                            ints(kv_len, "kv_len"), q_start ? ints(*q_start, "q_start") : nullptr};
+  const hkv_scores scores = {sm_scale, cap, causal ? 1 : 0, small(window, "window"),
+                             positions ? ints(*positions, "positions") : nullptr,
+                             begin ? ints(*begin, "begin") : nullptr,
+                             prefix_len ? ints(*prefix_len, "prefix_len") : nullptr,
+                             slopes ? static_cast<const float*>(slopes->data_ptr()) : nullptr};
+  if (make) {
+    const int64_t bytes = calls.attend_pages_bytes(&pool.shape, &req, small(n, "n_tokens"), qh.n_heads, pool.dtype);
+    if (bytes > 0) ws = made_on({bytes}, q.options().dtype(at::kByte), at_stream);
+  }
+  if (ws) need(ws->scalar_type() == at::kByte && ws->is_contiguous(), "workspace must be a contiguous uint8 tensor");
+  const hkv_heads oh = heads_of(out, "out");
+  const int st = launch(calls.attend_pages, &pool.shape, &pool.pages, &req, &qh, pool.dtype, small(n, "n_tokens"),
+                        &scores, &oh, static_cast<float*>(lse.data_ptr()), ws ? ws->data_ptr() : nullptr,
+                        ws ? ws->numel() : 0, at_stream.stream());
+  return py::make_tuple(st, out, lse);
+}
+
+py::tuple join_attention(const Tensor& out_a, const Tensor& lse_a, const Tensor& out_b, const Tensor& lse_b,
+                         const Maybe& out_, const Maybe& lse_, const py::object& stream) {
+  OneGpu on("join_attention");
+  on(out_a)(lse_a)(out_b)(lse_b)(out_)(lse_);
+  const auto at_stream = stream_of(stream, on.device());
+  const hkv_heads ah = heads_of(out_a, "out_a"), bh = heads_of(out_b, "out_b");
+  const Tensor out = out_ ? *out_ : made_on(out_a.sizes(), out_a.options(), at_stream);
+  const hkv_heads oh = heads_of(out, "out");
+  need(out_b.sizes() == out_a.sizes() && out.sizes() == out_a.sizes() &&
+           out_b.scalar_type() == out_a.scalar_type() && out.scalar_type() == out_a.scalar_type(),
+       "out_a, out_b and out must share shape and dtype");
+  const int64_t n = out_a.size(0), h = out_a.size(1);
+  const Tensor lse = lse_ ? *lse_ : made_on({n, h}, lse_a.options().dtype(at::kFloat), at_stream);
+  for (const Tensor* t : {&lse_a, &lse_b, &lse})
+    need(t->dim() == 2 && t->size(0) == n && t->size(1) == h && t->scalar_type() == at::kFloat && t->is_contiguous(),
+         "lse_a, lse_b and lse must be contiguous float32 [n_tokens, n_heads] tensors");
+  const int st = launch(calls.join, &ah, static_cast<const float*>(lse_a.data_ptr()), &bh,
+                        static_cast<const float*>(lse_b.data_ptr()), dtype_of(out_a), small(n, "n_tokens"), &oh,
+                        static_cast<float*>(lse.data_ptr()), at_stream.stream());
+  return py::make_tuple(st, out, lse);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_native, m) {
@@ -376,4 +525,7 @@ PYBIND11_MODULE(_native, m) {
   m.def("append_tokens", &append_tokens);
   m.def("attend_records", &attend_records);
   m.def("fetch", &fetch);
+  m.def("append_pages", &append_pages);
+  m.def("attend_pages", &attend_pages);
+  m.def("join_attention", &join_attention);
 }

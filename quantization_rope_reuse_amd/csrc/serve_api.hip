@@ -20,24 +20,6 @@ bool aligned(const void* p, unsigned bytes) {
 
 int to_status(hipError_t e) { return e == hipSuccess ? HKV_OK : HKV_ERR_HIP; }
 
-// Rows of head vectors; `data` may be NULL where nothing is addressed.
-int check_heads(const hkv_heads* h, int32_t dtype, int32_t n_tokens, HeadView* v) {
-  const int es = hkv::element_size(dtype);
-  if (!h || es == 0 || h->n_heads < 0 || n_tokens < 0) return HKV_ERR_INVALID_ARG;
-  for (int64_t s : {h->token_stride, h->head_stride}) {
-    if (s < 0 || s > INT64_MAX / 8 || (s * es) % 16 != 0) return HKV_ERR_INVALID_ARG;
-  }
-  if (!aligned(h->data, 16)) return HKV_ERR_INVALID_ARG;
-  if (!h->data && h->n_heads > 0 && n_tokens > 0) return HKV_ERR_INVALID_ARG;
-  v->data = static_cast<char*>(h->data);
-  v->token = h->token_stride * es;
-  v->head = h->head_stride * es;
-  v->n_heads = h->n_heads;
-  if (!hkv::span_ok({{n_tokens, v->token}, {h->n_heads, v->head}}, int64_t{HKV_HEAD_DIM} * es))
-    return HKV_ERR_INVALID_ARG;
-  return HKV_OK;
-}
-
 // One layer's pool of records; an empty one addresses nothing, so its base
 // may be NULL.
 int check_pool(const hkv_shape* shape, int32_t fmt, const hkv_records* records, Geometry* g,
@@ -54,8 +36,30 @@ int check_pool(const hkv_shape* shape, int32_t fmt, const hkv_records* records, 
   return hkv::records_check(records, fmt, shape, v);
 }
 
+}  // namespace
+
+namespace hkv {
+
+// Rows of head vectors; `data` may be NULL where nothing is addressed.
+int heads_check(const hkv_heads* h, int32_t dtype, int32_t n_tokens, HeadView* v) {
+  const int es = element_size(dtype);
+  if (!h || es == 0 || h->n_heads < 0 || n_tokens < 0) return HKV_ERR_INVALID_ARG;
+  for (int64_t s : {h->token_stride, h->head_stride}) {
+    if (s < 0 || s > INT64_MAX / 8 || (s * es) % 16 != 0) return HKV_ERR_INVALID_ARG;
+  }
+  if (!aligned(h->data, 16)) return HKV_ERR_INVALID_ARG;
+  if (!h->data && h->n_heads > 0 && n_tokens > 0) return HKV_ERR_INVALID_ARG;
+  v->data = static_cast<char*>(h->data);
+  v->token = h->token_stride * es;
+  v->head = h->head_stride * es;
+  v->n_heads = h->n_heads;
+  if (!span_ok({{n_tokens, v->token}, {h->n_heads, v->head}}, int64_t{HKV_HEAD_DIM} * es))
+    return HKV_ERR_INVALID_ARG;
+  return HKV_OK;
+}
+
 // Sizes of the requests of an attention call (pointers apart).
-int check_requests(const hkv_requests* r, const Geometry& g, int32_t n_tokens, int32_t n_q_heads) {
+int requests_check(const hkv_requests* r, const Geometry& g, int32_t n_tokens, int32_t n_q_heads) {
   if (!r || r->n_requests < 0 || r->max_blocks < 0 || r->max_queries < 1 || n_tokens < 0 ||
       r->table_stride < r->max_blocks)
     return HKV_ERR_INVALID_ARG;
@@ -64,11 +68,27 @@ int check_requests(const hkv_requests* r, const Geometry& g, int32_t n_tokens, i
   if (g.n_heads > 4096) return HKV_ERR_UNSUPPORTED;                      // grid.x limit
   if (static_cast<int64_t>(r->max_blocks) * g.block_tokens > INT32_MAX) return HKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(n_tokens) * n_q_heads > INT32_MAX) return HKV_ERR_UNSUPPORTED;
-  if (!hkv::span_ok({{r->n_requests, r->table_stride}}, r->max_blocks)) return HKV_ERR_INVALID_ARG;
+  if (!span_ok({{r->n_requests, r->table_stride}}, r->max_blocks)) return HKV_ERR_INVALID_ARG;
   return HKV_OK;
 }
 
-}  // namespace
+// The axes of a rotation and the positions of its tokens.
+int rope_check(const hkv_rope_axes* rope, const int32_t* positions, int64_t axis_stride,
+               int32_t n_tokens) {
+  if (!rope || rope->n_axes < 1 || rope->n_axes > 8) return HKV_ERR_INVALID_ARG;
+  if (rope->pairs != HKV_ROPE_INTERLEAVED && rope->pairs != HKV_ROPE_HALF_SPLIT)
+    return HKV_ERR_INVALID_ARG;
+  if (!(rope->rope_base > 0.0) || !isfinite(rope->rope_base)) return HKV_ERR_INVALID_ARG;
+  for (int i = 0; i < HKV_HEAD_DIM / 2; ++i)
+    if (rope->axis[i] < -1 || rope->axis[i] >= rope->n_axes || rope->freq[i] > 127)
+      return HKV_ERR_INVALID_ARG;
+  if (axis_stride < 0 || !span_ok({{rope->n_axes, axis_stride}}, n_tokens) ||
+      !aligned(positions, 4))
+    return HKV_ERR_INVALID_ARG;
+  return HKV_OK;
+}
+
+}  // namespace hkv
 
 extern "C" {
 
@@ -107,23 +127,15 @@ int hkv_rope_heads(const hkv_rope_axes* rope, const int32_t* positions, int64_t 
                    int32_t n_tokens, const hkv_heads* q, const hkv_heads* k,
                    const hkv_heads* q_out, const hkv_heads* k_out, int32_t dtype,
                    int32_t inverse, hipStream_t stream) {
-  if (!rope || rope->n_axes < 1 || rope->n_axes > 8) return HKV_ERR_INVALID_ARG;
-  if (rope->pairs != HKV_ROPE_INTERLEAVED && rope->pairs != HKV_ROPE_HALF_SPLIT)
-    return HKV_ERR_INVALID_ARG;
-  if (!(rope->rope_base > 0.0) || !isfinite(rope->rope_base)) return HKV_ERR_INVALID_ARG;
-  for (int i = 0; i < HKV_HEAD_DIM / 2; ++i)
-    if (rope->axis[i] < -1 || rope->axis[i] >= rope->n_axes || rope->freq[i] > 127)
-      return HKV_ERR_INVALID_ARG;
+  const int axes = hkv::rope_check(rope, positions, axis_stride, n_tokens);
+  if (axes != HKV_OK) return axes;
   HeadView v[4];
   const hkv_heads* heads[4] = {q, k, q_out, k_out};
   for (int i = 0; i < 4; ++i) {
-    const int st = check_heads(heads[i], dtype, n_tokens, &v[i]);
+    const int st = hkv::heads_check(heads[i], dtype, n_tokens, &v[i]);
     if (st != HKV_OK) return st;
   }
   if (q->n_heads != q_out->n_heads || k->n_heads != k_out->n_heads) return HKV_ERR_INVALID_ARG;
-  if (axis_stride < 0 || !hkv::span_ok({{rope->n_axes, axis_stride}}, n_tokens) ||
-      !aligned(positions, 4))
-    return HKV_ERR_INVALID_ARG;
   const int64_t vecs = static_cast<int64_t>(q->n_heads) + k->n_heads;
   if (vecs > (1 << 24) || static_cast<int64_t>(n_tokens) * vecs > INT32_MAX)
     return HKV_ERR_UNSUPPORTED;
@@ -141,8 +153,8 @@ int hkv_append_tokens(const hkv_shape* shape, int32_t fmt, const hkv_heads* k, c
   HeadView kv, vv;
   int st;
   if ((st = check_pool(shape, fmt, dst, &g, &rv)) != HKV_OK) return st;
-  if ((st = check_heads(k, dtype, n_tokens, &kv)) != HKV_OK) return st;
-  if ((st = check_heads(v, dtype, n_tokens, &vv)) != HKV_OK) return st;
+  if ((st = hkv::heads_check(k, dtype, n_tokens, &kv)) != HKV_OK) return st;
+  if ((st = hkv::heads_check(v, dtype, n_tokens, &vv)) != HKV_OK) return st;
   if (k->n_heads != g.n_heads || v->n_heads != g.n_heads) return HKV_ERR_INVALID_ARG;
   if (static_cast<int64_t>(n_tokens) * g.n_heads > INT32_MAX) return HKV_ERR_UNSUPPORTED;
   if (!aligned(slots, 8)) return HKV_ERR_INVALID_ARG;
@@ -155,7 +167,7 @@ int64_t hkv_attend_workspace_bytes(const hkv_shape* shape, const hkv_requests* r
                                    int32_t n_tokens, int32_t n_q_heads, int32_t dtype) {
   Geometry g;
   if (hkv::shape_check(shape, &g) != HKV_OK || g.n_layers != 1 || hkv::element_size(dtype) == 0 ||
-      check_requests(requests, g, n_tokens, n_q_heads) != HKV_OK)
+      hkv::requests_check(requests, g, n_tokens, n_q_heads) != HKV_OK)
     return -1;
   return hkv::attend_workspace_bytes(g, *requests, n_tokens, n_q_heads, dtype);
 }
@@ -168,10 +180,10 @@ int hkv_attend_records(const hkv_shape* shape, int32_t fmt, const hkv_records* r
   hkv::AttendCall c;
   int st;
   if ((st = check_pool(shape, fmt, records, &c.g, &c.rec)) != HKV_OK) return st;
-  if ((st = check_heads(q, dtype, n_tokens, &c.q)) != HKV_OK) return st;
-  if ((st = check_heads(out, dtype, n_tokens, &c.out)) != HKV_OK) return st;
+  if ((st = hkv::heads_check(q, dtype, n_tokens, &c.q)) != HKV_OK) return st;
+  if ((st = hkv::heads_check(out, dtype, n_tokens, &c.out)) != HKV_OK) return st;
   if (q->n_heads != out->n_heads) return HKV_ERR_INVALID_ARG;
-  if ((st = check_requests(requests, c.g, n_tokens, q->n_heads)) != HKV_OK) return st;
+  if ((st = hkv::requests_check(requests, c.g, n_tokens, q->n_heads)) != HKV_OK) return st;
   if (!requests->q_start && requests->n_requests != n_tokens) return HKV_ERR_INVALID_ARG;
   if (!isfinite(static_cast<float>(sm_scale))) return HKV_ERR_INVALID_ARG;
   c.delta = nullptr;

@@ -15,6 +15,14 @@ struct HeadView {          // byte addressing of rows of head vectors
 
 constexpr int32_t kMaxStepRequests = 4096;
 
+// Checks shared by the C entry points: rows of head vectors (`data` may be
+// NULL where nothing is addressed), the sizes of an attention call's requests
+// (pointers apart), and a rotation's axes and positions (which may be NULL).
+int heads_check(const hkv_heads* h, int32_t dtype, int32_t n_tokens, HeadView* v);
+int requests_check(const hkv_requests* r, const Geometry& g, int32_t n_tokens, int32_t n_q_heads);
+int rope_check(const hkv_rope_axes* rope, const int32_t* positions, int64_t axis_stride,
+               int32_t n_tokens);
+
 hipError_t launch_plan(const hkv_step& s, hipStream_t stream);
 
 hipError_t launch_rope(const hkv_rope_axes& rope, const int32_t* positions, int64_t axis_stride,

@@ -1,5 +1,6 @@
-"""Thin binding of libhkv (include/hkv.h, include/hkv_serve.h): ctypes, and
-csrc/binding.cpp for the fetch and the serving calls.
+"""Thin binding of libhkv (include/hkv.h, include/hkv_serve.h,
+include/hkv_pages.h): ctypes, and csrc/binding.cpp for the fetch and the
+serving calls.
 
 Argument marshalling only: every step of put, CRC and fetch runs in the HIP
 kernels of libhkv.so.  torch is used for device memory and streams: tensors
@@ -103,6 +104,14 @@ class KeyShift(ctypes.Structure):
                 ("pairs", ctypes.c_int32)]
 
 
+# Structure of include/hkv_pages.h.
+
+class Scores(ctypes.Structure):
+    _fields_ = [("sm_scale", ctypes.c_double), ("cap", ctypes.c_double), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("positions", ctypes.c_void_p), ("begin", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
+
+
 _lib = None
 _native = _native_of = None
 
@@ -199,6 +208,18 @@ def lib():
         for name in ("hkv_plan_step", "hkv_rope_heads", "hkv_append_tokens",
                      "hkv_attend_records"):
             getattr(l, name).restype = ctypes.c_int
+        l.hkv_append_pages.argtypes = [
+            P(Shape), P(RopeAxes), vp, ctypes.c_int64, P(Heads), P(Heads), P(Heads), P(Heads),
+            ctypes.c_int32, ctypes.c_int32, vp, P(Pages), ctypes.c_int32, vp]
+        l.hkv_attend_pages.argtypes = [
+            P(Shape), P(Pages), P(Requests), P(Heads), ctypes.c_int32, ctypes.c_int32, P(Scores),
+            P(Heads), vp, vp, ctypes.c_int64, vp]
+        l.hkv_attend_pages_workspace_bytes.argtypes = l.hkv_attend_workspace_bytes.argtypes
+        l.hkv_attend_pages_workspace_bytes.restype = ctypes.c_int64
+        l.hkv_join_attention.argtypes = [P(Heads), vp, P(Heads), vp, ctypes.c_int32,
+                                         ctypes.c_int32, P(Heads), vp, vp]
+        for name in ("hkv_append_pages", "hkv_attend_pages", "hkv_join_attention"):
+            getattr(l, name).restype = ctypes.c_int
         l.hkv_record_bytes.argtypes = [ctypes.c_int32] * 4
         l.hkv_record_bytes.restype = ctypes.c_int64
         l.hkv_status_string.argtypes = [ctypes.c_int32]
@@ -210,7 +231,8 @@ def lib():
 # The library's calls that binding.cpp makes.
 NATIVE_CALLS = ("hkv_plan_step", "hkv_rope_heads", "hkv_append_tokens", "hkv_attend_records",
                 "hkv_attend_workspace_bytes", "hkv_fetch_dequant_rope_shift",
-                "hkv_fetch_dequant_rope_shift_tokens", "hkv_record_bytes")
+                "hkv_fetch_dequant_rope_shift_tokens", "hkv_record_bytes", "hkv_append_pages",
+                "hkv_attend_pages", "hkv_attend_pages_workspace_bytes", "hkv_join_attention")
 
 
 def native():
@@ -883,4 +905,72 @@ def attend_records(q, records, fmt, block_tokens: int, n_kv_heads: int, block_ta
         HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, causal, delta_m, rope_base,
         PAIRS[pairs], out, lse, workspace, stream)
     _check("hkv_attend_records", st)
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Serving from pages (include/hkv_pages.h)
+# ---------------------------------------------------------------------------
+
+def append_pages(k, v, slots, k_pages, v_pages, positions=None, rope_base=None, pairs="half_split",
+                 sections=(HEAD_DIM // 2,), order="blocked", freq=None, q=None, q_out=None,
+                 stream=None):
+    """Write the new tokens' keys and values, [n_tokens, n_kv_heads, 128] each,
+    to slots (int64 [n_tokens]; page * block_tokens + token, negative to skip)
+    of one layer's pages [P, T_b, H, 128].  With positions (int32 [n_tokens],
+    or [n_axes, n_tokens]) and rope_base the keys turn on the way, and q
+    [n_tokens, n_q_heads, 128], if given, turns into q_out (which may be q), as
+    in rope_heads.  The pages may have another dtype than k and v.  Returns
+    q_out (None without q)."""
+    axes = 0 if rope_base is None else _axes_address(
+        float(rope_base), pairs, tuple(sections), order if isinstance(order, str) else tuple(order),
+        None if freq is None else tuple(freq))[0]
+    st, q_out = native().append_pages(k, v, slots, k_pages, v_pages, positions, axes, q, q_out, stream)
+    _check("hkv_append_pages", st)
+    return q_out
+
+
+def attend_pages_workspace_bytes(num_pages: int, block_tokens: int, n_kv_heads: int,
+                                 n_requests: int, max_blocks: int, n_tokens: int, n_q_heads: int,
+                                 max_queries: int, dtype) -> int:
+    shape = Shape(1, num_pages, block_tokens, n_kv_heads, HEAD_DIM)
+    req = Requests(n_requests, max_blocks, max_queries, None, max_blocks, None, None)
+    return int(lib().hkv_attend_pages_workspace_bytes(
+        ctypes.byref(shape), ctypes.byref(req), n_tokens, n_q_heads, TORCH_DTYPES[dtype]))
+
+
+def attend_pages(q, k_pages, v_pages, block_table, kv_len, q_start=None, max_queries=None,
+                 sm_scale=None, causal: bool = True, positions=None, begin=None, prefix_len=None,
+                 window=None, cap=None, slopes=None, out=None, lse=None, workspace=True,
+                 stream=None):
+    """Attention of q [n_tokens, n_q_heads, 128] over one layer's pages [P, T_b,
+    H, 128] of the same dtype; returns (out, lse), lse float32 [n_tokens,
+    n_q_heads].  Rows that belong to no request (padding) are not written: a
+    tensor that the call makes is not initialised there.
+    block_table, kv_len, q_start, max_queries, workspace: as attend_records
+    takes them, the table's entries pages (workspace of
+    attend_pages_workspace_bytes bytes).  Query j of n of a request stands at
+    kv_len - n + j, or at its entry of positions (int32 [n_tokens]; negative:
+    sees nothing), and sees the cached tokens before prefix_len (int32
+    [n_requests]) and those from begin (int32 [n_tokens]: the first token of its
+    document) on that lie up to it (causal) and less than `window` before it.
+    cap: scores become cap * tanh(score / cap); slopes (float32 [n_q_heads]):
+    the head's slope times the distance is taken off.  sm_scale: 1 / sqrt(128)
+    if None."""
+    st, out, lse = native().attend_pages(
+        q, k_pages, v_pages, block_table, kv_len, q_start,
+        -1 if max_queries is None else max(int(max_queries), 0),
+        HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, causal, positions, begin, prefix_len,
+        0 if window is None else window, 0.0 if cap is None else cap, slopes, out, lse, workspace,
+        stream)
+    _check("hkv_attend_pages", st)
+    return out, lse
+
+
+def join_attention(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
+    """Two attentions of the same queries over different tokens, each an
+    output [n_tokens, n_heads, 128] and its lse, made that over all of them:
+    (out, lse).  out may be out_a or out_b, lse lse_a or lse_b."""
+    st, out, lse = native().join_attention(out_a, lse_a, out_b, lse_b, out, lse, stream)
+    _check("hkv_join_attention", st)
     return out, lse
