@@ -76,14 +76,19 @@ struct PageSpan {        // a request's queries and cached tokens
   int len, pre;          // pre: tokens of the prefix
 };
 
+// (An array that is not there is read elsewhere, so that the loads need not
+// wait for each other.)
 __device__ __forceinline__ PageSpan page_span(const PageAttendParams& p, int r) {
+  const int32_t* bounds = p.q_start ? p.q_start + r : p.kv_len;
+  const int32_t* prefix = p.prefix ? p.prefix : p.kv_len;
+  const int from = bounds[0], to = p.q_start ? bounds[1] : 0, len = p.kv_len[r], pre = prefix[r];
   PageSpan s;
-  s.start = p.q_start ? min(max(p.q_start[r], 0), p.n_tokens) : r;
-  const int end = p.q_start ? min(max(p.q_start[r + 1], 0), p.n_tokens) : r + 1;
+  s.start = p.q_start ? min(max(from, 0), p.n_tokens) : r;
+  const int end = p.q_start ? min(max(to, 0), p.n_tokens) : r + 1;
   s.n_q = max(end - s.start, 0);
   s.rows = min(s.n_q, p.max_queries) * p.group;
-  s.len = min(max(p.kv_len[r], 0), p.max_len);
-  s.pre = p.prefix ? min(max(p.prefix[r], 0), s.len) : 0;
+  s.len = min(max(len, 0), p.max_len);
+  s.pre = p.prefix ? min(max(pre, 0), s.len) : 0;
   return s;
 }
 
@@ -196,7 +201,8 @@ __device__ __forceinline__ f32x16 mma(s8 a, s8 b, f32x16 c) {
 
 // A copy of x that the compiler takes for a new value: what is computed from
 // it stays where it stands instead of holding registers across a loop.
-__device__ __forceinline__ int here(int x) {
+template <class T>
+__device__ __forceinline__ T here(T x) {
   asm volatile("" : "+v"(x));
   return x;
 }
@@ -227,6 +233,19 @@ __device__ __forceinline__ f32x16 score_tile(const char* keys, const Queries<DT>
     for (int kk = 0; kk < 8; ++kk) acc = mma<DT>(k[kk], q.x[kk], acc);
   }
   return acc;
+}
+
+// Two weights rounded to the type, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_two(float x, float y) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  if constexpr (DT == kBF16) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x, y}), b2));
+  } else {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x, y}), h2));
+  }
 }
 
 // 8 weights as an operand, and (PP = 2) what rounding them left out.
@@ -341,6 +360,7 @@ struct RowsState {
   f32x16 o[4];
   float m, l;        // the reference; this lane's part of the sum
   bool far;          // some row's reference is
+  float scale, shift;  // of the tile at hand: weights are exp2(scale x + shift)
 };
 
 // Bits of the tokens that a row sees of a tile of up to 64 from `first` on, of
@@ -353,32 +373,44 @@ __device__ __forceinline__ uint64_t seen_of(const Sight& v, uint64_t live, int f
   return (live & (below(v.pre) | (below(v.hi) & ~below(v.lo)))) >> (4 * h);
 }
 
-// The weights of a tile of N subtiles from its products.  part: some row may
-// not see all of it; seen: what the lane's row sees of it (seen_of); from_first:
-// the row's position, counted from the token of register 0.
-template <int DT, int PP, bool CAP, bool BIAS, int N>
-__device__ __forceinline__ void weigh_tile(f32x16 (&acc)[N], Weights<DT, PP> (&out)[N], RowsState& st,
-                                           const ScoreScale& f, float from_first, bool part, uint64_t seen) {
-  constexpr float kOff = PageTraits<DT>::kOff, kSlack = PageTraits<DT>::kSlack;
-  constexpr bool kPlain = !CAP && !BIAS;
-  if constexpr (!kPlain) {
+// The largest of a tile's products, once the scores are made of them that have
+// a cap or a bias (the others stay products).  from_first: the row's position,
+// counted from the token of register 0.
+template <bool CAP, bool BIAS, int N>
+__device__ __forceinline__ float scores_of(f32x16 (&acc)[N], const ScoreScale& f, float from_first) {
+  if constexpr (CAP || BIAS) {
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         acc[u][i] = score_of<CAP, BIAS>(acc[u][i], f, fabsf(from_first - (kSub * u + 8 * (i >> 2) + (i & 3))));
   }
-  if (part) {
-#pragma unroll
-    for (int u = 0; u < N; ++u)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[u][i] = (seen >> (kSub * u + 8 * (i >> 2) + (i & 3))) & 1 ? acc[u][i] : -INFINITY;
-  }
   float top = -INFINITY;
 #pragma unroll
   for (int u = 0; u < N; ++u)
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, acc[u][i]);
+  return top;
+}
+
+// Masks a tile's scores (part: some row may not see all of it; seen: what the
+// lane's row sees of it, see seen_of), moves the reference where they outgrow it
+// and says how they become weights.
+template <int DT, bool CAP, bool BIAS, int N>
+__device__ __forceinline__ void refer_tile(f32x16 (&acc)[N], float top, RowsState& st, const ScoreScale& f,
+                                           bool part, uint64_t seen) {
+  constexpr float kOff = PageTraits<DT>::kOff, kSlack = PageTraits<DT>::kSlack;
+  constexpr bool kPlain = !CAP && !BIAS;
+  if (part) {
+    top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        acc[u][i] = (seen >> (kSub * u + 8 * (i >> 2) + (i & 3))) & 1 ? acc[u][i] : -INFINITY;
+        top = fmaxf(top, acc[u][i]);
+      }
+  }
   if constexpr (kPlain) top *= f.scale;            // (scale > 0)
   if (__any(top > st.m + kSlack)) {
     top = fmaxf(top, __shfl_xor(top, 32));
@@ -390,31 +422,31 @@ __device__ __forceinline__ void weigh_tile(f32x16 (&acc)[N], Weights<DT, PP> (&o
     for (int d = 0; d < 4; ++d) st.o[d] *= keep;
     st.far = __any(fabsf(m) >= kFar && m != kNoReference);
   }
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-    float w[16];
-    if (!kPlain || st.far) {
-      // the reference came from rounded scores: so do the weights
+  st.scale = kPlain ? f.scale : 1.0f;
+  st.shift = kOff - st.m;
+  if (kPlain && st.far) {
+    // the reference came from rounded scores: so do the weights
 #pragma clang fp contract(off)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float s = kPlain ? acc[u][i] * f.scale : acc[u][i];
-        w[i] = (s - st.m) + kOff;
-      }
-    } else {
-      const float shift = kOff - st.m;
+    for (int u = 0; u < N; ++u)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = __builtin_fmaf(acc[u][i], f.scale, shift);
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      w[i] = __builtin_amdgcn_exp2f(w[i]);
-      sum += w[i];
-    }
-    st.l += sum;
-    out[u].set(w);
+      for (int i = 0; i < 16; ++i) acc[u][i] = acc[u][i] * f.scale - st.m;
+    st.scale = 1.0f;
+    st.shift = kOff;
   }
+}
+
+// The weights of a subtile and their sum.
+template <int DT, int PP>
+__device__ __forceinline__ float weigh_tile(const f32x16& acc, Weights<DT, PP>& out, const RowsState& st) {
+  float w[16], sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i], st.scale, st.shift));
+    sum += w[i];
+  }
+  out.set(w);
+  return sum;
 }
 
 // 16 bytes per lane straight into LDS: lane i's to `to` + 16 i.
@@ -422,6 +454,53 @@ __device__ __forceinline__ void bring16(const char* from, char* to) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(from),
                                    (__attribute__((address_space(3))) uint32_t*)(to), 16, 0, 0);
 }
+
+// What a wave brings at once: the keys or values of a group of tokens, 4 loads.
+// In LDS they lie as in Row; the first token of a group is a multiple of kTokens.
+template <int DT>
+struct Group {
+  using R = Row<DT>;
+  static constexpr int kLoads = 4;
+  static constexpr int kTokens = kLoads * R::kPerWave;
+
+  // This lane's part of a load of a whole group: its row's offset, and its
+  // chunk's place, which load n moves by bits of its own.
+  struct Lane {
+    uint32_t row_off, place;
+    __device__ __forceinline__ Lane(const PageAttendParams& p, bool key, int first, int lane) {
+      const int row = lane / R::kChunks, chunk = lane % R::kChunks;
+      row_off = static_cast<uint32_t>(row) * static_cast<uint32_t>(p.token);
+      place = (key ? R::key(first + row, chunk) : R::value(first + row, chunk)) << 4;
+    }
+  };
+  static __device__ __forceinline__ uint32_t turn(bool key, int n) {
+    return 16 * (key ? R::kPerWave * n : R::value(R::kPerWave * n, 0));
+  }
+  // Load n; `rows` is the first of the group's tokens.
+  static __device__ __forceinline__ void bring_one(const PageAttendParams& p, const char* rows, const Lane& lane, bool key,
+                                                   int n, char* to) {
+    const uint32_t off = here(lane.row_off) + (here(lane.place) ^ turn(key, n));
+    bring16(rows + n * (R::kPerWave * p.token) + off, to + 16 * kWave * n);
+  }
+
+  // Groups whose tokens lie apart or do not all exist: `at` is the place of
+  // token lane % kTokens, -1 if it does not exist.
+  static __device__ __forceinline__ int64_t place(const PageAttendParams& p, int token, int len, int entry, int64_t head_off) {
+    const bool known = token < len && static_cast<uint32_t>(entry) < static_cast<uint32_t>(p.num_pages);
+    return known ? entry * p.page + (token - block_of(p, token) * p.block_tokens) * p.token + head_off : int64_t{-1};
+  }
+  static __device__ __forceinline__ void bring_apart(const char* from, int64_t at, bool key, int first, char* to, int lane) {
+    const int row = lane / R::kChunks, chunk = lane % R::kChunks;
+    const char* none = reinterpret_cast<const char*>(kZeros);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int t = R::kPerWave * n + row;
+      const int64_t off = __shfl(at, t);
+      bring16(off < 0 ? none : from + off + ((key ? R::key(first + t, chunk) : R::value(first + t, chunk)) << 4),
+              to + 16 * kWave * n);
+    }
+  }
+};
 
 // Waits until at most N of the wave's loads are under way (they arrive in
 // order), and for its LDS reads.  Nothing moves across.

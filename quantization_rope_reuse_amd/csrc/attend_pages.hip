@@ -6,98 +6,111 @@
 namespace hkv {
 namespace {
 
-// One workgroup per row that more than one range worked on: its waves (up to
-// 8, by how many partial results a row may have) take the partial results in
-// turn, a lane two dims; then the waves join in order.  Partial outputs are
-// divided by their sums, so that no product here leaves their range.
-constexpr int kJoinMost = 8;
+// Joins the partial results of rows that more than one workgroup worked on.
+// 16 lanes, 8 dims each, take a row's partial results in turn; where these are
+// many, `sets` (1, 2, 4 .. 16) such lane groups take every sets-th of them and
+// join in LDS, in order.  Partial outputs are divided by their sums, so that
+// no product here leaves their range.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinLanes = kHeadDim / 8;
+constexpr int kJoinGroups = kJoinThreads / kJoinLanes;
 
-__global__ __launch_bounds__(kJoinMost * kWave) void page_join_kernel(PageAttendParams p, int elem, int waves) {
-  const int r = blockIdx.y;
-  const PageSpan s = page_span(p, r);
-  const int j = blockIdx.x / p.q_heads;
-  if (j >= min(s.n_q, p.max_queries)) return;
-  const int head = blockIdx.x - j * p.q_heads;
-  const int kh = head / p.group;
-  // The partial results of this row, w0 .. w1: of the ranges that its item
-  // reaches over (one alone wrote the result), or the chunk kernel's cuts.
-  int w0 = 0, w1 = p.splits - 1;
-  uint32_t f0 = 0, per = 0;
-  int in_item = 0;
-  if (p.splits == 0) {
-    const int row = j * p.group + (head - kh * p.group);
-    const int item = row / kItemRows;
-    const uint32_t first = p.prefix_out[r];
-    const uint32_t tiles = (p.prefix_out[r + 1] - first) / ((s.rows + kItemRows - 1) / kItemRows);
-    f0 = first + item * tiles;
-    per = p.prefix_out[p.n_requests + 1];
-    w0 = f0 / per;
-    w1 = (f0 + tiles - 1) / per;
-    if (w0 == w1) return;
-    in_item = row - item * kItemRows;
-  }
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
-  auto at = [&](int w) {
-    if (p.splits > 0)
-      return (static_cast<int64_t>(w) * p.n_tokens + s.start + j) * p.q_heads + head;
-    const int which = w == w0 && f0 > w0 * per ? 1 : 0;
-    return (static_cast<int64_t>(w * 2 + which) * p.n_heads + kh) * p.part_rows + in_item;
-  };
-  float m = kNoReference, l = 0.0f;
-  float2 o = make_float2(0.0f, 0.0f);      // divided by l
-  for (int w = w0 + wave; w <= w1; w += waves) {
-    const int64_t i = at(w);
-    const float2 ml = p.part_ml[i];
-    const float2 x = reinterpret_cast<const float2*>(p.part_o + i * kHeadDim)[lane];
-    const float top = fmaxf(m, ml.x);
+struct Joined {
+  float m, l, o[8];                        // o divided by l
+  __device__ __forceinline__ void add(float x_m, float x_l, const float (&x)[8]) {
+    const float top = fmaxf(m, x_m);
     const float keep = l * (m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top));
-    const float more = ml.y * (ml.x == top ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top));
+    const float more = x_l * (x_m == top ? 1.0f : __builtin_amdgcn_exp2f(x_m - top));
     const float sum = keep + more;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const float a = keep * inv, b = more * inv;
-    o.x = (keep == 0.0f ? 0.0f : a * o.x) + (more == 0.0f ? 0.0f : b * x.x);
-    o.y = (keep == 0.0f ? 0.0f : a * o.y) + (more == 0.0f ? 0.0f : b * x.y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = (keep == 0.0f ? 0.0f : a * o[i]) + (more == 0.0f ? 0.0f : b * x[i]);
     m = top;
     l = sum;
   }
-  __shared__ float2 join_ml[kJoinMost];
-  __shared__ float2 join_o[kJoinMost][kWave];
-  join_o[wave][lane] = o;
-  if (lane == 0) join_ml[wave] = make_float2(m, l);
-  __syncthreads();
-  if (threadIdx.x >= kHeadDim / 8) return;     // 8 dims a lane
-  float top = kNoReference, sum = 0.0f, y[8] = {};
-  for (int w = 0; w < waves; ++w) top = fmaxf(top, join_ml[w].x);
-  for (int w = 0; w < waves; ++w)
-    sum += join_ml[w].y * (join_ml[w].x == top ? 1.0f : __builtin_amdgcn_exp2f(join_ml[w].x - top));
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  for (int w = 0; w < waves; ++w) {
-    const float f = join_ml[w].y * (join_ml[w].x == top ? 1.0f : __builtin_amdgcn_exp2f(join_ml[w].x - top)) * inv;
-    if (f == 0.0f) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = join_o[w][4 * threadIdx.x + i];
-      y[2 * i] += a.x * f;
-      y[2 * i + 1] += a.y * f;
+};
+
+__global__ __launch_bounds__(kJoinThreads) void page_join_kernel(PageAttendParams p, int elem, int sets) {
+  const int r = blockIdx.y;
+  const int group = threadIdx.x / kJoinLanes, lane = threadIdx.x % kJoinLanes;
+  const int set = group % sets;
+  const PageSpan s = page_span(p, r);
+  const int queries = min(s.n_q, p.max_queries);
+  const int64_t row_head = static_cast<int64_t>(blockIdx.x) * (kJoinGroups / sets) + group / sets;
+  const int j = static_cast<int>(row_head / p.q_heads);
+  const int head = static_cast<int>(row_head - static_cast<int64_t>(j) * p.q_heads);
+  const int kh = head / p.group;
+  const int64_t query = s.start + j;
+  // The partial results of this row, w0 .. w1: of the ranges that its item
+  // reaches over, or the chunk kernel's cuts; where w0 = w1, that one wrote the
+  // result.
+  int w0 = 0, w1 = 0;
+  uint32_t f0 = 0, per = 1;
+  int in_item = 0;
+  if (j < queries) {
+    if (p.splits > 0) {
+      w1 = p.part_n[query * p.q_heads + head] - 1;
+    } else {
+      const int row = j * p.group + (head - kh * p.group);
+      const int item = row / kItemRows;
+      const uint32_t first = p.prefix_out[r];
+      const uint32_t tiles = (p.prefix_out[r + 1] - first) / ((s.rows + kItemRows - 1) / kItemRows);
+      f0 = first + item * tiles;
+      per = p.prefix_out[p.n_requests + 1];
+      w0 = f0 / per;
+      w1 = (f0 + tiles - 1) / per;
+      in_item = row - item * kItemRows;
     }
   }
-  const int64_t query = s.start + j;
-  char* dst = p.out + query * p.o_token + head * p.o_head + 8 * threadIdx.x * elem;
+  auto at = [&](int w) {
+    if (p.splits > 0) return (static_cast<int64_t>(w) * p.n_tokens + query) * p.q_heads + head;
+    const int which = w == w0 && f0 > w0 * per ? 1 : 0;
+    return (static_cast<int64_t>(w * 2 + which) * p.n_heads + kh) * p.part_rows + in_item;
+  };
+  Joined y = {kNoReference, 0.0f, {}};
+  if (w0 < w1)
+    for (int w = w0 + set; w <= w1; w += sets) {
+      const int64_t i = at(w);
+      const float2 ml = p.part_ml[i];
+      const float4* o = reinterpret_cast<const float4*>(p.part_o + i * kHeadDim + 8 * lane);
+      const float4 a = o[0], b = o[1];
+      y.add(ml.x, ml.y, {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+    }
+  if (sets > 1) {
+    __shared__ float2 join_ml[kJoinGroups];
+    __shared__ float join_o[kJoinGroups][kHeadDim];
+    if (lane == 0) join_ml[group] = make_float2(y.m, y.l);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) join_o[group][i * kJoinLanes + lane] = y.o[i];
+    __syncthreads();
+    if (set != 0) return;
+    for (int w = 1; w < sets; ++w) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = join_o[group + w][i * kJoinLanes + lane];
+      y.add(join_ml[group + w].x, join_ml[group + w].y, x);
+    }
+  }
+  if (w0 == w1) return;
+  char* dst = p.out + query * p.o_token + head * p.o_head + 8 * lane * elem;
   if (elem == 4)
-    store8<kF32>(dst, y);
+    store8<kF32>(dst, y.o);
   else if (p.f16)
-    store8<kF16>(dst, y);
+    store8<kF16>(dst, y.o);
   else
-    store8<kBF16>(dst, y);
-  if (p.lse && threadIdx.x == 0) p.lse[query * p.q_heads + head] = lse_of(top, sum);
+    store8<kBF16>(dst, y.o);
+  if (p.lse && lane == 0) p.lse[query * p.q_heads + head] = lse_of(y.m, y.l);
 }
 
 }  // namespace
 
 int64_t attend_pages_workspace_bytes(const Geometry& g, const hkv_requests& req, int32_t n_tokens,
                                      int32_t n_q_heads, int dtype) {
-  return page_share_bytes(page_share_of(g, req, n_tokens, n_q_heads, dtype), req);
+  (void)dtype;
+  const int64_t even = page_share_bytes(page_share_of(g, req, n_tokens, n_q_heads, false));
+  const int64_t slanted = page_share_bytes(page_share_of(g, req, n_tokens, n_q_heads, true));
+  return even > slanted ? even : slanted;
 }
 
 hipError_t launch_attend_pages(const PageAttendCall& c, hipStream_t stream) {
@@ -115,6 +128,8 @@ hipError_t launch_attend_pages(const PageAttendCall& c, hipStream_t stream) {
   while ((int64_t{1} << s) < c.g.block_tokens) ++s;
   p.block_shift = 31 + s;
   p.block_magic = ((uint64_t{1} << p.block_shift) + c.g.block_tokens - 1) / c.g.block_tokens;
+  const int together = c.dtype == HKV_F32 ? Group<kF32>::kTokens : Group<kBF16>::kTokens;
+  p.grouped = c.g.block_tokens % together == 0 && c.pages.token < (int64_t{1} << 31) / 16;
   p.n_requests = c.req.n_requests;
   p.table = c.req.block_table;
   p.table_stride = c.req.table_stride;
@@ -149,15 +164,21 @@ hipError_t launch_attend_pages(const PageAttendCall& c, hipStream_t stream) {
   p.begin = c.scores.begin;
   p.prefix = c.scores.prefix_len;
 
-  const PageShare share = page_share_of(c.g, c.req, c.n_tokens, c.q.n_heads, c.dtype);
+  // rows that see very different numbers of tokens
+  const bool slanted = p.causal && p.window == 0 && !p.begin &&
+                       (p.positions || static_cast<int64_t>(p.max_queries) * 2 > p.max_len);
+  const PageShare share = page_share_of(c.g, c.req, c.n_tokens, c.q.n_heads, slanted);
   p.splits = share.splits;
   p.ranges = share.ranges;
   p.min_tiles = share.min_tiles;
   p.part_rows = share.part_rows;
   if (share.rows > 0) {
     char* ws = static_cast<char*>(c.workspace);
-    p.prefix_out = reinterpret_cast<uint32_t*>(ws);
-    ws += page_prefix_bytes(c.req);
+    if (share.splits > 0)
+      p.part_n = reinterpret_cast<int32_t*>(ws);
+    else
+      p.prefix_out = reinterpret_cast<uint32_t*>(ws);
+    ws += share.index_bytes;
     p.part_ml = reinterpret_cast<float2*>(ws);
     p.part_o = reinterpret_cast<float*>(ws + (share.rows * 8 + 15) / 16 * 16);
   }
@@ -183,16 +204,17 @@ hipError_t launch_attend_pages(const PageAttendCall& c, hipStream_t stream) {
   }
   if (e != hipSuccess || share.rows == 0) return e;
   const int64_t queries = c.req.max_queries < c.n_tokens ? c.req.max_queries : c.n_tokens;
-  // about 8 partial results of a row for each wave
+  // how many lane groups share a row: about four of its partial results each
   const int64_t parts = share.splits > 0
                             ? share.splits
                             : share.ranges / (static_cast<int64_t>(c.req.n_requests) * share.items);
-  int waves = 1;
-  while (waves < kJoinMost && waves * 8 < parts) waves *= 2;
+  int sets = 1;
+  while (sets < kJoinGroups && sets * 4 < parts) sets *= 2;
+  const int64_t rows_each = kJoinGroups / sets;
   hipLaunchKernelGGL(page_join_kernel,
-                     dim3(static_cast<unsigned>(queries * c.q.n_heads),
+                     dim3(static_cast<unsigned>((queries * c.q.n_heads + rows_each - 1) / rows_each),
                           static_cast<unsigned>(c.req.n_requests)),
-                     dim3(waves * kWave), 0, stream, p, element_size(c.dtype), waves);
+                     dim3(kJoinThreads), 0, stream, p, element_size(c.dtype), sets);
   return hipGetLastError();
 }
 

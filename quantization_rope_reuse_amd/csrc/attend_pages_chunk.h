@@ -1,40 +1,130 @@
 // Attention over pages for many query rows per key head (chunks of prompts,
 // rows picked for recomputing).
 //
-// A workgroup of 8 waves takes 256 rows of a key head, 32 a wave, and walks the
-// tokens that some of them see in tiles of 64, which all waves bring into LDS
-// together and each uses for its own rows; tiles are cut into ranges where
-// items are too few for the CUs.  The loads of the tiles to come are under way
-// while a tile is worked on; one barrier a tile.
+// A workgroup of 4 waves takes 128 rows of a key head, 32 a wave, and walks the
+// tokens that some of them see in tiles of 64 (fp32: 32), which each wave brings a
+// quarter of into LDS and uses whole for its own rows; one barrier a tile, behind
+// which the tile after next sets out.  Two workgroups fit a CU (80 KB of LDS, 256
+// registers a lane), so that one's barriers, first loads and last stores hide
+// behind the other's products.
+//
+// Bound by issue: a wave's matrix instructions take 14 ns each, and of the vector
+// work beside them (an exponential, a fused product, half a conversion, a sum and
+// half a maximum a score) only about half hides behind them; a wave alone on its
+// SIMD leaves the rest idle.  2,048 queries over 16,384 tokens (32 heads, 515
+// GFLOP) take 524 us, 0.98 PFLOP/s, where the same products by the library's
+// largest matrix product would take 410; 64 rows a wave with one wave a SIMD 780,
+// 8 waves sharing a tile (half the loads into LDS, one workgroup a CU) 540, but
+// 179 for 158 with prompts of documents, whose items are short.
 #pragma once
+
+#include <type_traits>
 
 #include "attend_pages.h"
 
 namespace hkv {
 
-template <int DT> constexpr int kRing = DT == kF32 ? 2 : 3;      // tiles in LDS
+template <int DT> constexpr int kChunkTile = DT == kF32 ? 32 : 64;     // tokens
+
+// Step of a tile in 16-bit types: the products of the next one beside the weights
+// of this one, then the output of this one beside the next's largest product
+// (without cap and bias).  Matrix and vector instructions of one wave overlap
+// only where they stand in turn, and reads of LDS only where they stand well
+// ahead, so both are set out by hand and kept in place.
+// bring(n), n = 0 .. 7: loads that set out in between.
+template <int DT, bool MAX, class Bring>
+__device__ __forceinline__ float tile_step(const f32x16 (&now)[2], RowsState& st, f32x16 (&next)[2], const char* next_keys,
+                                           const char* values, const Queries<DT>& q, int lane, Bring bring) {
+  constexpr int kSubBytes = kSub * Row<DT>::kBytes;
+  const int id = here(lane);
+  const int k_at = (id & 31) * Row<DT>::kBytes + (Row<DT>::key(id & 31, id >> 5) << 4);
+  const int i16 = id & 15, v_token = 4 * (id >> 5) + (i16 >> 2);
+  const int v_at = v_token * Row<DT>::kBytes + (Row<DT>::value(v_token, 2 * ((id >> 4) & 1) + ((i16 >> 1) & 1)) << 4) + 8 * (i16 & 1);
+  auto key = [&](int u, int kk) __attribute__((always_inline)) {
+    return *reinterpret_cast<const s8*>(next_keys + u * kSubBytes + (k_at ^ (kk << 5)));
+  };
+  auto value = [&](int u, int n) __attribute__((always_inline)) {      // n: 4 s + d
+    const char* at = values + u * kSubBytes + (v_at ^ ((n & 3) << 6)) + 16 * (n >> 2) * Row<DT>::kBytes;
+    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)(at));
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS4)(at + 8 * Row<DT>::kBytes));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  // (each operand's registers take the one 8 products later)
+  s8 a[8];
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) a[kk] = key(0, kk);
+  __builtin_amdgcn_sched_barrier(0);
+  // Weights two at a time, each stage of a pair one product behind the last, so
+  // that none waits for the one before it.
+  u32x4 w[2][2];                         // operands: 8 weights each
+  float sum = 0.0f, x[2], e[2] = {};
+  auto exponent = [&](int at) __attribute__((always_inline)) {
+    return __builtin_fmaf(now[at >> 4][at & 15], st.scale, st.shift);
+  };
+  x[0] = exponent(0);
+  x[1] = exponent(1);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    next[u] = f32x16{};
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const int pair = 8 * u + kk;
+      next[u] = mma<DT>(a[kk], q.x[kk], next[u]);
+      a[kk] = u == 0 ? key(1, kk) : value(0, kk);
+      const float y0 = here(__builtin_amdgcn_exp2f(x[0])), y1 = here(__builtin_amdgcn_exp2f(x[1]));
+      if (pair < 15) {
+        x[0] = here(exponent(2 * pair + 2));
+        x[1] = here(exponent(2 * pair + 3));
+      }
+      if (pair > 0) {
+        sum = here(sum + e[0]);
+        w[(pair - 1) >> 3][((pair - 1) >> 2) & 1][(pair - 1) & 3] = here(pack_two<DT>(e[0], e[1]));
+        sum = here(sum + e[1]);
+      }
+      e[0] = y0;
+      e[1] = y1;
+      if (kk == 3 || kk == 6) bring(2 * u + (kk == 6));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  w[1][1][3] = pack_two<DT>(e[0], e[1]);
+  sum += e[0] + e[1];
+  st.l += sum;
+  float top = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      st.o[n & 3] = mma<DT>(a[n], __builtin_bit_cast(s8, w[u][n >> 2]), st.o[n & 3]);
+      if (u == 0) a[n] = value(1, n);
+      if (n == 1 || n == 4) bring(4 + 2 * u + (n == 4));
+      if (MAX) top = here(fmaxf(top, fmaxf(next[u][2 * n], next[u][2 * n + 1])));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  return top;
+}
 
 template <int DT>
 struct PageChunkShared {
-  char tile[kRing<DT>][2][kPageChunkTile * Row<DT>::kBytes];     // keys, values
-  uint64_t live[kRing<DT>];            // tokens of the tile that exist
-  int bounds[kPageChunkWaves][3];
+  static constexpr int kTile = kChunkTile<DT>;
+  char keys[2][kTile * Row<DT>::kBytes];     // (before the first tile: what the waves see)
+  char values[3][kTile * Row<DT>::kBytes];
 };
 
 template <int DT, bool CAP, bool BIAS>
 __global__ __launch_bounds__(kPageChunkThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void page_chunk_kernel(PageAttendParams p) {
   constexpr int ES = ElemSize<DT>::value;
-  constexpr int N = kPageChunkTile / kSub;
+  constexpr int kTile = kChunkTile<DT>;
+  constexpr int N = kTile / kSub;
   using R = Row<DT>;
-  constexpr int kRows = kPageChunkTile / kPageChunkWaves;        // that a wave brings
-  constexpr int kLoads = kRows / R::kPerWave;
+  constexpr int kRows = Group<DT>::kTokens;              // that a wave brings
+  static_assert(kTile == kRows * kPageChunkWaves, "each wave brings a group");
   extern __shared__ __attribute__((aligned(16))) char lds[];
   PageChunkShared<DT>& sh = *reinterpret_cast<PageChunkShared<DT>*>(lds);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int q32 = lane & 31, h = lane >> 5;
-  const char* none = reinterpret_cast<const char*>(kZeros);
 
   const int kh = blockIdx.x % p.n_heads;
   const int rest = blockIdx.x / p.n_heads;
@@ -60,25 +150,29 @@ void page_chunk_kernel(PageAttendParams p) {
     Queries<DT> q;
     q.load(q_row, h, p.q_keep, p.q_flip);
     __syncthreads();                       // the last rows' LDS is free
+    int* bounds = reinterpret_cast<int*>(sh.keys);
     if (lane == 0) {
-      sh.bounds[wave][0] = view.pre_most;
-      sh.bounds[wave][1] = view.lo_least;
-      sh.bounds[wave][2] = view.hi_most;
+      bounds[3 * wave] = view.pre_most;
+      bounds[3 * wave + 1] = view.lo_least;
+      bounds[3 * wave + 2] = view.hi_most;
     }
     __syncthreads();
     int pre = 0, lo = INT32_MAX, hi = 0;
 #pragma unroll
     for (int w = 0; w < kPageChunkWaves; ++w) {
-      pre = max(pre, sh.bounds[w][0]);
-      lo = min(lo, sh.bounds[w][1]);
-      hi = max(hi, sh.bounds[w][2]);
+      pre = max(pre, bounds[3 * w]);
+      lo = min(lo, bounds[3 * w + 1]);
+      hi = max(hi, bounds[3 * w + 2]);
     }
+    __syncthreads();
     pre = __builtin_amdgcn_readfirstlane(pre);
     lo = __builtin_amdgcn_readfirstlane(lo);
     hi = __builtin_amdgcn_readfirstlane(hi);
-    const TileList list = tiles_of_view(pre, lo, hi, kPageChunkTile);
-    const int per = (list.count + p.splits - 1) / p.splits;
-    const int t0 = min(split * per, list.count);
+    const TileList list = tiles_of_view(pre, lo, hi, kTile);
+    const int per = max((list.count + p.splits - 1) / p.splits, p.min_tiles);
+    const int parts = max((list.count + per - 1) / per, 1);
+    if (split >= parts) continue;
+    const int t0 = split * per;
     const int t1 = min(t0 + per, list.count);
 
     RowsState st;
@@ -88,76 +182,138 @@ void page_chunk_kernel(PageAttendParams p) {
     st.l = 0.0f;
     st.far = false;
 
-    int entry = -1;
-    auto entry_of = [&](int t) __attribute__((always_inline)) {
-      const int token = list.at(t) * kPageChunkTile + kRows * wave + (here(lane) & (kRows - 1));
-      return token < s.len ? table[block_of(p, token)] : -1;
+    // Each wave brings 16 tokens (fp32: 8) of a tile's keys and of its values.  The
+    // table entries are read a tile ahead, each lane that of a token.
+    const int group0 = kRows * wave;
+    const typename Group<DT>::Lane key_lane(p, true, group0, lane), value_lane(p, false, group0, lane);
+    int entry;
+    auto find = [&](int t) __attribute__((always_inline)) {
+      const int token = list.at(t) * kTile + (here(lane) & (kTile - 1));
+      entry = table[block_of(p, min(token, s.len - 1))];
     };
-    // Tile t into `area`, from its table entries; and tile t + 1's entries set out.
-    auto bring = [&](int t, char* area, uint64_t* live) __attribute__((always_inline)) {
-      const int id = here(lane);
-      const int token = list.at(t) * kPageChunkTile + kRows * wave + (id & (kRows - 1));
+    auto keys_of = [&](int t) __attribute__((always_inline)) { return sh.keys[(t - t0) & 1] + group0 * R::kBytes; };
+    auto values_of = [&](int t) __attribute__((always_inline)) { return sh.values[(t - t0) % 3] + group0 * R::kBytes; };
+    // Which of the tile's tokens exist.  Where all of the group do and lie in one
+    // block, `rows` is their place, to be brought; else brings them, and it is -1.
+    auto place = [&](int t, int64_t& rows) __attribute__((always_inline)) -> uint64_t {
+      const int first = list.at(t) * kTile;
+      const int token = first + (here(lane) & (kTile - 1));
       const bool known = token < s.len && static_cast<uint32_t>(entry) < static_cast<uint32_t>(p.num_pages);
-      const int64_t at = known ? entry * p.page + (token - block_of(p, token) * p.block_tokens) * p.token + head_off
-                               : int64_t{-1};
       const uint64_t alive = __ballot(known);
-      if (id == 0) reinterpret_cast<uint8_t*>(live)[wave] = static_cast<uint8_t>(alive);
-      if (t + 1 < t1) entry = entry_of(t + 1);
-#pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        const int first = R::kPerWave * n + id / R::kChunks;
-        const int64_t off = __shfl(at, first);
-        const int to = kRows * wave + first;
-        char* keys = area + kRows * R::kBytes * wave + 16 * kWave * n;
-        char* values = keys + kPageChunkTile * R::kBytes;
-        bring16(off < 0 ? none : p.k + off + (R::key(to, id % R::kChunks) << 4), keys);
-        bring16(off < 0 ? none : p.v + off + (R::value(to, id % R::kChunks) << 4), values);
+      constexpr uint32_t kAll = (1u << kRows) - 1;
+      if (p.grouped && (static_cast<uint32_t>(alive >> group0) & kAll) == kAll) {
+        const int page = __builtin_amdgcn_readlane(entry, group0);
+        const int at = first + group0;
+        rows = page * p.page + (at - block_of(p, at) * p.block_tokens) * p.token + head_off;
+      } else {
+        rows = -1;
+        const int in = group0 + (here(lane) & (kRows - 1));
+        const int64_t at = Group<DT>::place(p, first + in, s.len, __shfl(entry, in), head_off);
+        Group<DT>::bring_apart(p.k, at, true, group0, keys_of(t), here(lane));
+        Group<DT>::bring_apart(p.v, at, false, group0, values_of(t), here(lane));
       }
+      return alive;
     };
-    auto work = [&](const char* tile, const uint64_t* live_at, int first) __attribute__((always_inline)) {
-      if (!view.some(first, kPageChunkTile)) return;
-      const uint64_t live = *live_at;
-      const uint64_t alive = static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(live >> 32))) << 32 |
-                             static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(live)));
-      f32x16 acc[N];
-#pragma unroll
-      for (int u = 0; u < N; ++u) acc[u] = score_tile<DT>(tile + u * kSub * R::kBytes, q, lane);
-      const bool part = alive != ~uint64_t{0} || !view.all(first, kPageChunkTile);
-      float from_first = 0.0f;
-      if constexpr (BIAS) from_first = static_cast<float>(static_cast<double>(sight.pos) - (first + 4 * h));
-      const uint64_t seen = part ? seen_of(sight, alive, first, h) : 0;
-      Weights<DT, 1> w[N];
-      weigh_tile<DT, 1, CAP, BIAS, N>(acc, w, st, f, from_first, part, seen);
-#pragma unroll
-      for (int u = 0; u < N; ++u)
-        output_tile<DT, 1>(tile + (kPageChunkTile + u * kSub) * R::kBytes, w[u], st.o, lane);
+    auto bring_some = [&](int64_t rows, int n, char* keys, char* values) __attribute__((always_inline)) {
+      if (n < 4)
+        Group<DT>::bring_one(p, p.k + rows, key_lane, true, n, keys);
+      else
+        Group<DT>::bring_one(p, p.v + rows, value_lane, false, n - 4, values);
     };
-    // (the areas do not overlap: reads of one need not wait for loads of another)
-    auto step = [&](int t, const char* __restrict__ now, const uint64_t* __restrict__ now_live,
-                    char* __restrict__ next, uint64_t* __restrict__ next_live) __attribute__((always_inline)) {
-      if (t + kRing<DT> - 1 < t1) bring(t + kRing<DT> - 1, next, next_live);
-      work(now, now_live, list.at(t) * kPageChunkTile);
+    auto from_first = [&](int t) {
+      return BIAS ? static_cast<float>(static_cast<double>(sight.pos) - (list.at(t) * kTile + 4 * h)) : 0.0f;
+    };
+    auto refer = [&](int t, f32x16 (&acc)[N], float top, uint64_t alive) __attribute__((always_inline)) {
+      const int first = list.at(t) * kTile;
+      const bool part = (alive << (64 - kTile)) != ~uint64_t{0} << (64 - kTile) || !view.all(first, kTile);
+      refer_tile<DT, CAP, BIAS, N>(acc, top, st, f, part, part ? seen_of(sight, alive, first, h) : 0);
+    };
+    // Step t: the scores of tile t + 1 and the weights and output of tile t, whose
+    // scores `now` holds; tile t + 2 sets out.  The areas do not overlap: reads of
+    // some need not wait for loads of others.
+    uint64_t live = 0;                     // of tile t + 1
+    auto step = [&](int t, f32x16 (&now)[N], f32x16 (&next)[N], const char* __restrict__ next_keys,
+                    const char* __restrict__ values, char* __restrict__ later_keys,
+                    char* __restrict__ later_values) __attribute__((always_inline)) {
+      int64_t rows = -1;
+      uint64_t later_live = 0;
+      if (t + 2 < t1) {
+        later_live = place(t + 2, rows);
+        find(min(t + 3, t1 - 1));
+      }
+      float top;
+      if constexpr (DT == kF32) {
+        if (rows >= 0) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n) bring_some(rows, n, later_keys, later_values);
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          next[u] = score_tile<DT>(next_keys + u * kSub * R::kBytes, q, lane);
+          Weights<DT, 1> w;
+          st.l += weigh_tile<DT, 1>(now[u], w, st);
+          output_tile<DT, 1>(values + u * kSub * R::kBytes, w, st.o, lane);
+        }
+        top = scores_of<CAP, BIAS, N>(next, f, from_first(t + 1));
+      } else {
+        top = tile_step<DT, !CAP && !BIAS>(now, st, next, next_keys, values, q, lane, [&](int n) __attribute__((always_inline)) {
+          if (rows >= 0) bring_some(rows, n, later_keys, later_values);
+        });
+        if (CAP || BIAS) top = scores_of<CAP, BIAS, N>(next, f, from_first(t + 1));
+      }
+      refer(t + 1, next, top, live);
+      live = later_live;
     };
     if (t0 < t1) {
-      entry = entry_of(t0);
+      f32x16 one[N], two[N];
+      // Keys of tile t0 + n lie in slot n % 2, values in slot n % 3.
+      find(t0);
+      uint64_t first_live = 0;
 #pragma unroll
-      for (int n = 0; n < kRing<DT> - 1; ++n)
-        if (t0 + n < t1) bring(t0 + n, sh.tile[n][0], &sh.live[n]);
-      int slot = 0;
-      for (int t = t0; t < t1; ++t) {
-        // this tile's loads; the next ones' may be under way (a ring of two has none)
-        if (kRing<DT> > 2 && t + 1 < t1)
-          wait_loads<2 * kLoads*(kRing<DT> - 2)>();
-        else
-          wait_loads<0>();
+      for (int n = 0; n < 2; ++n) {
+        if (t0 + n >= t1) break;
+        int64_t rows;
+        (n ? live : first_live) = place(t0 + n, rows);
+        find(min(t0 + n + 1, t1 - 1));
+        if (rows >= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) bring_some(rows, i, keys_of(t0 + n), values_of(t0 + n));
+        }
+      }
+      auto together = [&]() __attribute__((always_inline)) {
+        // the loads of the last step, and everybody's reads of what the next ones replace
+        wait_loads<0>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const int free_slot = slot == 0 ? kRing<DT> - 1 : slot - 1;
-        step(t, sh.tile[slot][0], &sh.live[slot], sh.tile[free_slot][0], &sh.live[free_slot]);
-        slot = slot + 1 == kRing<DT> ? 0 : slot + 1;
+      };
+      together();
+#pragma unroll
+      for (int u = 0; u < N; ++u) one[u] = score_tile<DT>(sh.keys[0] + u * kSub * R::kBytes, q, lane);
+      refer(t0, one, scores_of<CAP, BIAS, N>(one, f, from_first(t0)), first_live);
+      auto go = [&](int t, f32x16 (&now)[N], f32x16 (&next)[N]) __attribute__((always_inline)) {
+        together();
+        const int n = t - t0;
+        step(t, now, next, sh.keys[(n + 1) & 1], sh.values[n % 3], keys_of(t + 2), values_of(t + 2));
+      };
+      int t = t0;
+      for (; t + 2 < t1; t += 2) {
+        go(t, one, two);
+        go(t + 1, two, one);
+      }
+      if (t + 1 < t1) {
+        go(t, one, two);
+#pragma unroll
+        for (int u = 0; u < N; ++u) one[u] = two[u];
+      }
+      together();
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        Weights<DT, 1> w;
+        st.l += weigh_tile<DT, 1>(one[u], w, st);
+        output_tile<DT, 1>(sh.values[(t1 - 1 - t0) % 3] + u * kSub * R::kBytes, w, st.o, lane);
       }
     }
-    const WaveTiles mine = {list, t0, t1, 1, kPageChunkTile};
+    const WaveTiles mine = {list, t0, t1, 1, kTile};
     finish_rows<DT, CAP, BIAS>(p, table, head_off, q_row, sight, s.len, mine, st, f, lane);
 
     const int id = here(lane), last_h = id >> 5;
@@ -167,7 +323,7 @@ void page_chunk_kernel(PageAttendParams p) {
       const int last_head = kh * p.group + (last_row - last_j * p.group);
       const int64_t last_query = s.start + last_j;
       const int64_t at = last_query * p.q_heads + last_head;
-      const bool whole = p.splits == 1;
+      const bool whole = parts == 1;
       const int64_t part_row = split * static_cast<int64_t>(p.n_tokens) * p.q_heads + at;
       char* dst = whole ? p.out + last_query * p.o_token + last_head * p.o_head
                         : reinterpret_cast<char*>(p.part_o + part_row * kHeadDim);
@@ -183,6 +339,7 @@ void page_chunk_kernel(PageAttendParams p) {
             store4<kF32>(dst + dim * 4, z);
         }
       if (last_h == 0) {
+        if (p.splits > 1 && split == 0) p.part_n[at] = parts;
         if (!whole)
           p.part_ml[part_row] = make_float2(st.m, st.l);
         else if (p.lse)

@@ -11,10 +11,9 @@ constexpr int kPageRowsThreads = kPageRowsWaves * 64;
 constexpr int kPageRowsTile = 32;          // tokens
 constexpr int kMaxDealtRequests = 1024;    // requests whose tiles are dealt out evenly
 
-constexpr int kPageChunkWaves = 8;
+constexpr int kPageChunkWaves = 4;
 constexpr int kPageChunkThreads = kPageChunkWaves * 64;
 constexpr int kPageChunkRows = kPageChunkWaves * kItemRows;
-constexpr int kPageChunkTile = 64;         // tokens
 
 struct PageAttendParams {
   const char* k;
@@ -23,6 +22,7 @@ struct PageAttendParams {
   int32_t num_pages, block_tokens, n_heads;
   uint64_t block_magic;    // token / block_tokens = token * magic >> shift, token < 2^31
   int32_t block_shift;
+  int32_t grouped;         // groups of 16 (fp32: 8) tokens lie in one block, their offsets below 2^31
   int32_t n_requests;
   const int32_t* table;
   int64_t table_stride;
@@ -46,10 +46,11 @@ struct PageAttendParams {
   const int32_t* prefix;
   // how the work is shared out
   int32_t ranges;          // > 0: the rows kernel deals all tiles out over this many ranges
-  int32_t min_tiles;       // least tiles of a range
+  int32_t min_tiles;       // least tiles of a range or cut
   int32_t part_rows;       // rows per head of a partial result
-  int32_t splits;          // > 0: the chunk kernel runs, cutting each item's tiles
+  int32_t splits;          // > 0: the chunk kernel runs, cutting each item's tiles into up to so many
   uint32_t* prefix_out;    // [n_requests + 2]: first tile of each request, total, tiles per range
+  int32_t* part_n;         // [n_tokens][q_heads]: cuts of each row's item
   float2* part_ml;         // reference and sum of each partial row
   float* part_o;           // its output
 };

@@ -2,7 +2,7 @@
 // wave works on tiles of its own.
 //
 // An item is up to 32 rows of a key head.  The tiles of all items are dealt
-// out evenly over ranges, about two workgroups of four waves per CU; a
+// out evenly over ranges, about one workgroup of four waves per CU; a
 // workgroup's waves take a range's tiles in turn and join in LDS, and what
 // reaches over several ranges is joined by a second kernel.
 //
@@ -69,54 +69,81 @@ void page_rows_kernel(PageAttendParams p) {
 
   uint32_t at = 0, end = 0;            // dealt tiles
   int r = 0, item = range, items = 0;
+  const int n = p.n_requests;
+  const bool few = n <= kWave;         // a wave's lanes hold the requests' tiles
+  uint32_t run = 0;                    // tiles up to and with this lane's request
+  auto tiles_of = [&](int i) {
+    const PageSpan s = page_span(p, i);
+    return s.rows > 0 ? static_cast<uint32_t>((s.rows + kItemRows - 1) / kItemRows) * dealt_tiles(p, s).count : 0u;
+  };
+  // tiles before request i
+  auto before = [&](int i) -> uint32_t {
+    if (few) return i > 0 ? __builtin_amdgcn_readlane(run, i - 1) : 0;
+    return __builtin_amdgcn_readfirstlane(sh.prefix[i]);
+  };
   if (p.ranges > 0) {
-    const int n = p.n_requests;
-    const int per_thread = (n + kPageRowsThreads - 1) / kPageRowsThreads;
-    const int r0 = min(static_cast<int>(threadIdx.x) * per_thread, n);
-    const int r1 = min(r0 + per_thread, n);
-    auto tiles_of = [&](int i) {
-      const PageSpan s = page_span(p, i);
-      return static_cast<uint32_t>((s.rows + kItemRows - 1) / kItemRows) *
-             (s.rows > 0 ? dealt_tiles(p, s).count : 0);
-    };
-    uint32_t sum = 0;
-    for (int i = r0; i < r1; ++i) {
-      const uint32_t x = tiles_of(i);
-      sh.prefix[i + 1] = x;
-      sum += x;
-    }
-    uint32_t upto = sum;
+    if (few) {
+      // every wave for itself, without LDS or a barrier
+      run = lane < n ? tiles_of(lane) : 0;
+      if (n > 1) {
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const uint32_t x = __shfl_up(upto, off);
-      if (lane >= off) upto += x;
+        for (int off = 1; off < kWave; off <<= 1) {
+          const uint32_t x = __shfl_up(run, off);
+          if (lane >= off) run += x;
+        }
+      }
+    } else {
+      const int per_thread = (n + kPageRowsThreads - 1) / kPageRowsThreads;
+      const int r0 = min(static_cast<int>(threadIdx.x) * per_thread, n);
+      const int r1 = min(r0 + per_thread, n);
+      uint32_t sum = 0;
+      for (int i = r0; i < r1; ++i) {
+        const uint32_t x = tiles_of(i);
+        sh.prefix[i + 1] = x;
+        sum += x;
+      }
+      uint32_t upto = sum;
+#pragma unroll
+      for (int off = 1; off < kWave; off <<= 1) {
+        const uint32_t x = __shfl_up(upto, off);
+        if (lane >= off) upto += x;
+      }
+      if (lane == kWave - 1) sh.wave_sum[wave] = upto;
+      __syncthreads();
+      uint32_t sums = upto - sum;
+      for (int w = 0; w < wave; ++w) sums += sh.wave_sum[w];
+      for (int i = r0; i < r1; ++i) {
+        sums += sh.prefix[i + 1];
+        sh.prefix[i + 1] = sums;
+      }
+      if (threadIdx.x == 0) sh.prefix[0] = 0;
+      __syncthreads();
     }
-    if (lane == kWave - 1) sh.wave_sum[wave] = upto;
-    __syncthreads();
-    uint32_t before = upto - sum;
-    for (int w = 0; w < wave; ++w) before += sh.wave_sum[w];
-    for (int i = r0; i < r1; ++i) {
-      before += sh.prefix[i + 1];
-      sh.prefix[i + 1] = before;
-    }
-    if (threadIdx.x == 0) sh.prefix[0] = 0;
-    __syncthreads();
-    const uint32_t total = sh.prefix[n];
+    const uint32_t total = before(n);
     const uint32_t per = max((total + p.ranges - 1) / p.ranges, static_cast<uint32_t>(p.min_tiles));
     if (blockIdx.x == 0) {
-      for (int i = threadIdx.x; i <= n; i += kPageRowsThreads) p.prefix_out[i] = sh.prefix[i];
+      if (few) {
+        if (wave == 0 && lane < n) p.prefix_out[lane + 1] = run;
+        if (threadIdx.x == 0) p.prefix_out[0] = 0;
+      } else {
+        for (int i = threadIdx.x; i <= n; i += kPageRowsThreads) p.prefix_out[i] = sh.prefix[i];
+      }
       if (threadIdx.x == 0) p.prefix_out[n + 1] = per;
     }
     at = min(range * per, total);      // range * per < total + per * ranges: below 2^32
     end = min(at + per, total);
     if (at >= end) return;
-    int last = n;
-    while (last - r > 1) {
-      const int mid = (r + last) >> 1;
-      if (sh.prefix[mid] <= at)
-        r = mid;
-      else
-        last = mid;
+    if (few) {
+      r = __builtin_popcountll(__ballot(lane < n && run <= at));
+    } else {
+      int last = n;
+      while (last - r > 1) {
+        const int mid = (r + last) >> 1;
+        if (before(mid) <= at)
+          r = mid;
+        else
+          last = mid;
+      }
     }
   } else {
     r = blockIdx.y;
@@ -125,16 +152,15 @@ void page_rows_kernel(PageAttendParams p) {
 
   const uint32_t first_at = at;
   while (p.ranges > 0 ? at < end : item < items) {
-    PageSpan s = page_span(p, r);
-    if (p.ranges > 0) {
-      // (requests without rows have no tiles)
-      while (sh.prefix[r + 1] <= at) ++r;
-      s = page_span(p, r);
-    }
+    // (requests without rows have no tiles)
+    if (p.ranges > 0)
+      while (before(r + 1) <= at) ++r;
+    r = __builtin_amdgcn_readfirstlane(r);
+    const PageSpan s = page_span(p, r);
     const TileList list = dealt_tiles(p, s);
     int seg0 = 0, seg1 = list.count;
     if (p.ranges > 0) {
-      const uint32_t in = at - sh.prefix[r];
+      const uint32_t in = at - before(r);
       item = in / list.count;
       seg0 = in - item * list.count;
       seg1 = min(static_cast<uint32_t>(list.count), seg0 + (end - at));
@@ -226,7 +252,8 @@ void page_rows_kernel(PageAttendParams p) {
         if constexpr (BIAS) from_first = static_cast<float>(static_cast<double>(sight.pos) - (first + 4 * h));
         const uint64_t seen = part ? seen_of(sight, live, first, h) : 0;
         Weights<DT, PP> w[1];
-        weigh_tile<DT, PP, CAP, BIAS, 1>(acc, w, st, f, from_first, part, seen);
+        refer_tile<DT, CAP, BIAS, 1>(acc, scores_of<CAP, BIAS, 1>(acc, f, from_first), st, f, part, seen);
+        st.l += weigh_tile<DT, PP>(acc[0], w[0], st);
         if (next < seg1)
           wait_loads<kLoads>();            // the values; the next keys may be under way
         else

@@ -1,5 +1,6 @@
 // How the work of an attention call over pages is shared out (host code):
-// which kernel, ranges of tiles, cuts.
+// which kernel, ranges of tiles, cuts.  (Times: 32 query heads, 8 key heads,
+// bf16.)
 #pragma once
 
 #include "attend_pages_launch.h"
@@ -11,33 +12,49 @@ struct PageShare {
   int ranges, min_tiles, part_rows;
   int64_t rows;            // partial rows in all
   int64_t items;           // of one request, at most
+  int64_t index_bytes;     // of the workspace's first part
 };
 
+// slanted: the rows see very different numbers of tokens.
 inline PageShare page_share_of(const Geometry& g, const hkv_requests& req, int32_t n_tokens,
-                               int32_t n_q_heads, int dtype) {
+                               int32_t n_q_heads, bool slanted) {
   PageShare s = {};
   const int64_t queries = req.max_queries < n_tokens ? req.max_queries : n_tokens;
   const int64_t group = n_q_heads / g.n_heads;
   const int64_t rows = queries * group;
+  const int64_t all_rows = n_tokens * group;
   const int64_t max_len = static_cast<int64_t>(req.max_blocks) * g.block_tokens;
-  // Where requests have fewer rows on average than one of the chunk kernel's
-  // workgroups, most of its workgroups would hold little: up to where the
-  // join's workgroups, one for every row that a request might have, cost what
-  // that spares, such steps take the rows kernel.
-  const bool sparse = static_cast<int64_t>(n_tokens) * group < static_cast<int64_t>(kPageChunkRows) * req.n_requests &&
-                      queries * n_q_heads * req.n_requests <= (1 << 19);
-  if (rows > 128 && !sparse) {
-    // One workgroup per 256 rows and key head; their tiles are cut where
-    // these are too few for the CUs.
+  // The rows kernel where requests have few rows on average: 16 requests over
+  // 2,000 tokens with 16 queries (64 rows) each take 49 us by it and 42 by the
+  // chunk kernel, with 40 queries 87 and 53.  Also where the step as a whole is
+  // small, up to 256 rows a request: 4 requests over 600 tokens with 40 queries
+  // each 17 and 24, 16 of them 31 and 25.  Both up to where the join's lanes, 16
+  // for every row that a request might have, cost what that spares.
+  const bool few_rows = all_rows < int64_t{64} * req.n_requests;
+  const bool small = all_rows < int64_t{256} * req.n_requests && max_len <= 1024 &&
+                     all_rows * g.n_heads * max_len < 10'000'000;
+  if (rows >= 64 && !((few_rows || small) && queries * n_q_heads * req.n_requests <= (1 << 19))) {
+    // Two workgroups fit a CU.  Where the items, 128 rows of a key head each, are
+    // too few for all CUs, their tiles are cut: 400 queries over 8,192 tokens take
+    // 81 us with cuts for 512 workgroups, 109 with those for 256.  Where some rows
+    // see far more than others, into twice as many, so that the short ones fill
+    // up, unless the cuts would be shorter than 2,048 tokens: 1,229 of 8,192
+    // tokens in the order of their positions take 182 us (305 uncut), a prompt
+    // of 2,048 tokens 79 (59 uncut).
     s.items = (rows + kPageChunkRows - 1) / kPageChunkRows;
-    int64_t most = static_cast<int64_t>(n_tokens) * group / kPageChunkRows + req.n_requests;
+    int64_t most = all_rows / kPageChunkRows + req.n_requests;
     const int64_t all = req.n_requests * s.items;
     most = (most < all ? most : all) * g.n_heads;
-    const int64_t cuts = 256 / (most < 1 ? 1 : most);
-    const int64_t long_enough = max_len / 512;
+    most = most < 1 ? 1 : most;
+    const int64_t cuts = (slanted ? 1024 : 512) / most;
+    const int64_t long_enough = max_len / (slanted ? 2048 : 512);
+    s.min_tiles = 8;
     s.splits = static_cast<int>(cuts < long_enough ? cuts : long_enough);
     s.splits = s.splits < 1 ? 1 : s.splits;
-    s.rows = s.splits > 1 ? static_cast<int64_t>(s.splits) * n_tokens * n_q_heads : 0;
+    if (s.splits > 1) {
+      s.rows = static_cast<int64_t>(s.splits) * n_tokens * n_q_heads;
+      s.index_bytes = (static_cast<int64_t>(n_tokens) * n_q_heads * 4 + 15) / 16 * 16;
+    }
     return s;
   }
   const int64_t tiles = max_len < kPageRowsTile ? 1 : (max_len + kPageRowsTile - 1) / kPageRowsTile;
@@ -46,26 +63,27 @@ inline PageShare page_share_of(const Geometry& g, const hkv_requests& req, int32
   s.part_rows = static_cast<int>(rows < kItemRows ? rows : kItemRows);
   const int64_t all = static_cast<int64_t>(req.n_requests) * s.items * tiles;
   // Requests of few tiles keep them to one workgroup per head and spare the
-  // join, unless there are too few of them to keep more than a few CUs at work.
+  // join, unless there are too few of them to keep more than a few CUs at work:
+  // 64 requests over 1,000 tokens take 41 us so and 58 with ranges, one over 777
+  // tokens 20 and 16.
   const int64_t few = static_cast<int64_t>(req.n_requests) * g.n_heads >= 32 ? 32 : 16;
   if (req.n_requests <= kMaxDealtRequests && tiles > few && queries * n_q_heads <= (1 << 20) &&
       all < (int64_t{1} << 30)) {
-    int64_t ranges = 512 / g.n_heads;
+    // One workgroup per CU: 512 instead of 256 take 127 us for 111 (32 requests of
+    // up to 8,192 tokens, 64 query heads), 95 for 77 (16 of up to 4,096, 5 queries
+    // each, fp32).
+    int64_t ranges = 256 / g.n_heads;
     const int64_t most = (all + s.min_tiles - 1) / s.min_tiles;
     ranges = ranges < 1 ? 1 : ranges;
     s.ranges = static_cast<int>(ranges < most ? ranges : most);
   }
   s.rows = static_cast<int64_t>(s.ranges) * 2 * g.n_heads * s.part_rows;
-  (void)dtype;
+  s.index_bytes = (static_cast<int64_t>(req.n_requests + 2) * 4 + 15) / 16 * 16;
   return s;
 }
 
-inline int64_t page_prefix_bytes(const hkv_requests& req) {
-  return (static_cast<int64_t>(req.n_requests + 2) * 4 + 15) / 16 * 16;
-}
-
-inline int64_t page_share_bytes(const PageShare& s, const hkv_requests& req) {
-  return s.rows > 0 ? page_prefix_bytes(req) + (s.rows * 8 + 15) / 16 * 16 + s.rows * HKV_HEAD_DIM * 4 : 0;
+inline int64_t page_share_bytes(const PageShare& s) {
+  return s.rows > 0 ? s.index_bytes + (s.rows * 8 + 15) / 16 * 16 + s.rows * HKV_HEAD_DIM * 4 : 0;
 }
 
 }  // namespace hkv
