@@ -39,7 +39,7 @@ inline PageShare page_share_of(const Geometry& g, const hkv_requests& req, int32
     // 81 us with cuts for 512 workgroups, 109 with those for 256.  Where some rows
     // see far more than others, into twice as many, so that the short ones fill
     // up, unless the cuts would be shorter than 2,048 tokens: 1,229 of 8,192
-    // tokens in the order of their positions take 182 us (305 uncut), a prompt
+    // tokens in the order of their positions, capped, take 182 us (305 uncut), a prompt
     // of 2,048 tokens 79 (59 uncut).
     s.items = (rows + kPageChunkRows - 1) / kPageChunkRows;
     int64_t most = all_rows / kPageChunkRows + req.n_requests;
