@@ -327,17 +327,33 @@ void page_chunk_kernel(PageAttendParams p) {
       const int64_t part_row = split * static_cast<int64_t>(p.n_tokens) * p.q_heads + at;
       char* dst = whole ? p.out + last_query * p.o_token + last_head * p.o_head
                         : reinterpret_cast<char*>(p.part_o + part_row * kHeadDim);
+      if (DT != kF32 && whole) {
+        if constexpr (DT != kF32) {
+          // Lanes q and q + 32 exchange halves: 8 dims in a row, 16 bytes, for each.
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
+          for (int d = 0; d < 4; ++d)
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int dim = 32 * d + 8 * a + 4 * last_h;
-          const float z[4] = {st.o[d][4 * a], st.o[d][4 * a + 1], st.o[d][4 * a + 2], st.o[d][4 * a + 3]};
-          if (whole)
-            store4<DT>(dst + dim * ES, z);
-          else
-            store4<kF32>(dst + dim * 4, z);
+            for (int a = 0; a < 4; a += 2) {
+              uint32_t z[4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int at_a = 4 * a + 2 * i, at_b = at_a + 4;
+                const auto both = __builtin_amdgcn_permlane32_swap(pack_two<DT>(st.o[d][at_a], st.o[d][at_a + 1]),
+                                                                   pack_two<DT>(st.o[d][at_b], st.o[d][at_b + 1]), false, false);
+                z[i] = both[0];
+                z[2 + i] = both[1];
+              }
+              *reinterpret_cast<u32x4*>(dst + (32 * d + 8 * (a + last_h)) * ES) = u32x4{z[0], z[1], z[2], z[3]};
+            }
         }
+      } else {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+            store4<kF32>(dst + (32 * d + 8 * a + 4 * last_h) * 4,
+                         {st.o[d][4 * a], st.o[d][4 * a + 1], st.o[d][4 * a + 2], st.o[d][4 * a + 3]});
+      }
       if (last_h == 0) {
         if (p.splits > 1 && split == 0) p.part_n[at] = parts;
         if (!whole)
