@@ -14,6 +14,7 @@ namespace {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinLanes = kHeadDim / 8;
 constexpr int kJoinGroups = kJoinThreads / kJoinLanes;
+static_assert(kJoinGroups == kJoinMostSets, "a workgroup's lane groups");
 
 struct Joined {
   float m, l, o[8];                        // o divided by l
@@ -214,15 +215,7 @@ hipError_t launch_attend_pages(const PageAttendCall& c, hipStream_t stream) {
   }
   if (e != hipSuccess || share.rows == 0) return e;
   const int64_t queries = c.req.max_queries < c.n_tokens ? c.req.max_queries : c.n_tokens;
-  // How many lane groups share a row: about two of its partial results each, or
-  // four where there are many rows (one request over 4,000 tokens, 32 heads: 18.4
-  // us of both kernels for 19.4 with all in one; 400 queries over 8,192: 82 for 85).
-  const int64_t each = share.splits > 0 ? 4 : 2;
-  const int64_t parts = share.splits > 0
-                            ? share.splits
-                            : share.ranges / (static_cast<int64_t>(c.req.n_requests) * share.items);
-  int sets = 1;
-  while (sets < kJoinGroups && sets * each < parts) sets *= 2;
+  const int sets = page_join_sets(share, c.req.n_requests);
   const int64_t rows_each = kJoinGroups / sets;
   hipLaunchKernelGGL(page_join_kernel,
                      dim3(static_cast<unsigned>((queries * c.q.n_heads + rows_each - 1) / rows_each),

@@ -1,0 +1,82 @@
+"""Attention over pages by every way its work is shared out (the calls of
+attend_pages_paths.py, whose paths test_attend_pages_share.py holds) against
+the oracle in 64 bits: ranges, cuts that leave some rows whole, joins of few and
+many partial results."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from attend_pages_paths import CASES, ident  # noqa: E402
+from quantization_rope_reuse_amd import hkv  # noqa: E402
+from test_gpu_pages import check, ints, setup  # noqa: E402
+
+
+def made(case, seed):
+    """Pages, table, queries; positions of the requests' rows, in order, the first of them 0."""
+    dtype, tb, h, group, lens, asks, own, share = case
+    g, kp, vp, table, q_start, q = setup((dtype, tb, h, group, lens, asks, "tokens"), seed)
+    positions = None
+    if own:
+        positions = np.concatenate([np.sort(np.append(0, 1 + g.permutation(max(n, a) - 1)[:a - 1]))
+                                    for n, a in zip(lens, asks)])
+    return g, kp, vp, table, q_start, q, dict(positions=positions), share[0] == "chunk"
+
+
+@pytest.mark.parametrize("case", CASES, ids=ident)
+def test_paths(case):
+    print("paths", case, flush=True)
+    lens, most = case[4], max(case[5])
+    g, kp, vp, table, q_start, q, kw, one_part = made(case, 11)
+    check(q, kp, vp, table, lens, q_start, "causal", one_part, max_queries=most, **kw)
+    slopes = np.where(np.arange(q.shape[1]) % 2, 0.01, -0.0001)
+    check(q, kp, vp, table, lens, q_start, "cap, slopes", one_part, max_queries=most, cap=9.0, slopes=slopes, **kw)
+    check(q, kp, vp, table, lens, q_start, "window", one_part, max_queries=most, window=max(lens) // 3, **kw)
+    n = q.shape[0]
+    check(q, kp, vp, table, lens, q_start, "documents", one_part, max_queries=most, begin=g.integers(0, max(lens), n),
+          prefix_len=g.integers(0, 40, len(lens)), **kw)
+    check(q, kp, vp, table, lens, q_start, "all tokens", one_part, max_queries=most, causal=False)
+
+
+@pytest.mark.parametrize("case", CASES, ids=ident)
+def test_paths_with_holes(case):
+    """Entries left out, and pages that no entry names full of NaN."""
+    print("paths with holes", case, flush=True)
+    dtype, tb, h, group, lens, asks, own, share = case
+    g, kp, vp, table, q_start, q, kw, one_part = made(case, 12)
+    named = np.zeros(kp.shape[0], bool)
+    for r, n in enumerate(lens):
+        held = -(-n // tb)
+        out = g.random(held) < 0.3
+        table[r, :held][out] = np.where(g.random(out.sum()) < 0.5, -1, kp.shape[0])
+        inside = table[r, :held]
+        named[inside[(inside >= 0) & (inside < kp.shape[0])]] = True
+    for x in (kp, vp):
+        x[torch.from_numpy(~named).to(x.device)] = float("nan")
+    check(q, kp, vp, table, lens, q_start, "holes", one_part, max_queries=max(asks), **kw)
+
+
+@pytest.mark.parametrize("case", CASES, ids=ident)
+def test_workspace(case):
+    """A workspace of just the bytes asked for, full of NaN or of what the last
+    call left: the same bits, and nothing written behind it."""
+    print("workspace", case, flush=True)
+    dtype, tb, h, group, lens, asks, own, share = case
+    _, kp, vp, table, q_start, q, kw, _ = made(case, 13)
+    pos = None if kw["positions"] is None else ints(kw["positions"])
+    need = hkv.attend_pages_workspace_bytes(kp.shape[0], tb, h, len(lens), table.shape[1], q.shape[0], q.shape[1],
+                                            max(asks), q.dtype)
+    # (sizes alone decide the bytes: another call of them may be cut where this is not)
+    assert need > 0 or share in (("rows", 0, 1), ("chunk", 1))
+    args = (q, kp, vp, ints(table), ints(lens), ints(q_start))
+    a, la = hkv.attend_pages(*args, max_queries=max(asks), positions=pos)
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device=q.device)
+    for _ in range(2):
+        b, lb = hkv.attend_pages(*args, max_queries=max(asks), positions=pos, workspace=ws[:need])
+        assert torch.equal(a, b) and torch.equal(la, lb)
+        assert (ws[need:] == 0xFF).all()
