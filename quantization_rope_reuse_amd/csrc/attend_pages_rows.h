@@ -11,7 +11,7 @@
 // output, so that one or both are always under way and no wave waits for
 // another.  Memory bounds it (fp32: the matrix instructions): loads of random
 // 64-token pages into LDS reach 5.7 TB/s on this card; 32 requests of up to 8,192
-// tokens (64 heads over 8, bf16, 473 MB) take 97 to 111 us, 4.3 to 4.9 TB/s, one of
+// tokens (64 heads over 8, bf16, 473 MB) take 95 to 109 us, 4.3 to 5.0 TB/s, one of
 // 65,519 54 (5.0), the rest setting out, and passing from a request to the next.
 // Two workgroups a CU take 127, table entries read for groups of tokens 124.
 #pragma once
@@ -42,6 +42,15 @@ __device__ __forceinline__ TileList dealt_tiles(const PageAttendParams& p, const
   TileList t = tiles_of_view(s.pre, lo, hi, kPageRowsTile);
   t.count = max(t.count, 1);               // rows that see nothing are written all the same
   return t;
+}
+
+// Tiles are dealt by the turns of a workgroup's waves: an item's last turn may
+// have fewer tiles than waves.  (Ranges that begin inside a turn pass from an item
+// to the next more often: five drafts over 900 tokens, two items, take 23 us so for
+// 16, 16 requests of up to 4,096 with five each in fp32 78 for 70.)
+__device__ __forceinline__ int in_turns(int tiles) {
+  static_assert((kPageRowsWaves & (kPageRowsWaves - 1)) == 0, "a mask");
+  return (tiles + kPageRowsWaves - 1) & ~(kPageRowsWaves - 1);
 }
 
 template <int DT>
@@ -78,7 +87,7 @@ void page_rows_kernel(PageAttendParams p) {
   uint32_t run = 0;                    // tiles up to and with this lane's request
   auto tiles_of = [&](int i) {
     const PageSpan s = page_span(p, i);
-    return s.rows > 0 ? static_cast<uint32_t>((s.rows + kItemRows - 1) / kItemRows) * dealt_tiles(p, s).count : 0u;
+    return s.rows > 0 ? static_cast<uint32_t>((s.rows + kItemRows - 1) / kItemRows) * in_turns(dealt_tiles(p, s).count) : 0u;
   };
   // tiles before request i
   auto before = [&](int i) -> uint32_t {
@@ -124,7 +133,7 @@ void page_rows_kernel(PageAttendParams p) {
       __syncthreads();
     }
     const uint32_t total = before(n);
-    const uint32_t per = max((total + p.ranges - 1) / p.ranges, static_cast<uint32_t>(p.min_tiles));
+    const uint32_t per = in_turns(max((total + p.ranges - 1) / p.ranges, static_cast<uint32_t>(p.min_tiles)));
     if (blockIdx.x == 0) {
       if (few) {
         if (wave == 0 && lane < n) p.prefix_out[lane + 1] = run;
@@ -162,14 +171,16 @@ void page_rows_kernel(PageAttendParams p) {
     r = __builtin_amdgcn_readfirstlane(r);
     const PageSpan s = page_span(p, r);
     const TileList list = dealt_tiles(p, s);
-    int seg0 = 0, seg1 = list.count;
+    int seg0 = 0, seg1 = list.count, dealt = 0;
+    bool whole = true;
     if (p.ranges > 0) {
-      const uint32_t in = at - before(r);
-      item = in / list.count;
-      seg0 = in - item * list.count;
-      seg1 = min(static_cast<uint32_t>(list.count), seg0 + (end - at));
+      const uint32_t in = at - before(r), tiles = in_turns(list.count);
+      item = in / tiles;
+      seg0 = in - item * tiles;
+      dealt = min(tiles - seg0, end - at);
+      seg1 = min(seg0 + dealt, list.count);
+      whole = dealt == static_cast<int>(tiles);
     }
-    const bool whole = seg0 == 0 && seg1 == list.count;
     const int32_t* table = p.table + r * p.table_stride;
 
     const int row = min(item * kItemRows + q32, s.rows - 1);
@@ -337,7 +348,7 @@ void page_rows_kernel(PageAttendParams p) {
     }
     __syncthreads();                     // the tiles' LDS is free
     if (p.ranges > 0)
-      at += seg1 - seg0;
+      at += dealt;
     else
       item += gridDim.x / p.n_heads;
   }

@@ -58,15 +58,16 @@ inline PageShare page_share_of(const Geometry& g, const hkv_requests& req, int32
     return s;
   }
   const int64_t tiles = max_len < kPageRowsTile ? 1 : (max_len + kPageRowsTile - 1) / kPageRowsTile;
+  const int64_t turns = (tiles + kPageRowsWaves - 1) / kPageRowsWaves;     // of a workgroup's waves
   s.items = (rows + kItemRows - 1) / kItemRows;
   s.min_tiles = kPageRowsWaves;
   s.part_rows = static_cast<int>(rows < kItemRows ? rows : kItemRows);
-  const int64_t all = static_cast<int64_t>(req.n_requests) * s.items * tiles;
-  // Requests of few tiles keep them to one workgroup per head and spare the
-  // join, unless there are too few of them to keep more than a few CUs at work:
-  // 64 requests over 1,000 tokens take 41 us so and 58 with ranges, one over 777
-  // tokens 20 and 16.
-  const int64_t few = static_cast<int64_t>(req.n_requests) * g.n_heads >= 32 ? 32 : 16;
+  const int64_t all = static_cast<int64_t>(req.n_requests) * s.items * turns * kPageRowsWaves;
+  // Items of few tiles keep them to one workgroup and spare the join, unless
+  // there are too few items to keep more than a few CUs at work: 64 requests over
+  // up to 1,000 tokens take 41 us so and 57 with ranges, 8 over 777 21.5 and 23, 4
+  // 21.6 and 17, one 20 and 16.
+  const int64_t few = static_cast<int64_t>(req.n_requests) * s.items * g.n_heads >= 64 ? 32 : 16;
   if (req.n_requests <= kMaxDealtRequests && tiles > few && queries * n_q_heads <= (1 << 20) &&
       all < (int64_t{1} << 30)) {
     // One workgroup per CU: 512 instead of 256 take 127 us for 111 (32 requests of

@@ -8,9 +8,9 @@ CASES = [
     # few rows: whole items; ranges whose results 1, 2 .. 16 lane groups join
     ("bf16", 64, 8, 4, [900, 1] * 8, [1, 2] * 8, False, ("rows", 0, 1)),
     ("f16", 16, 8, 4, [600], [1], False, ("rows", 5, 4)),
-    ("f32", 7, 4, 7, [600, 0, 900], [5, 5, 5], False, ("rows", 44, 4)),
+    ("f32", 7, 4, 7, [600, 0, 900], [5, 5, 5], False, ("rows", 48, 4)),
     ("bf16", 64, 1, 8, [4000], [1], False, ("rows", 32, 16)),
-    ("f16", 16, 2, 3, [2000] * 7, [1] * 7, False, ("rows", 111, 8)),
+    ("f16", 16, 2, 3, [2000] * 7, [1] * 7, False, ("rows", 112, 8)),
     ("bf16", 32, 64, 1, [700] * 9, [1] * 9, False, ("rows", 0, 1)),
     # up to 256 rows a request, a small step
     ("f16", 16, 2, 4, [500, 90, 700], [40, 60, 30], False, ("rows", 128, 4)),
