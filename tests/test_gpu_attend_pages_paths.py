@@ -6,15 +6,13 @@ from __future__ import annotations
 
 import numpy as np
 import pytest
+import torch
+
+from attend_pages_paths import CASES, ident
+from quantization_rope_reuse_amd import hkv
+from test_gpu_pages import check, ints, setup
 
 pytestmark = pytest.mark.gpu
-torch = pytest.importorskip("torch")
-if not torch.cuda.is_available():
-    pytest.skip("needs a GPU", allow_module_level=True)
-
-from attend_pages_paths import CASES, ident  # noqa: E402
-from quantization_rope_reuse_amd import hkv  # noqa: E402
-from test_gpu_pages import check, ints, setup  # noqa: E402
 
 
 def made(case, seed):
