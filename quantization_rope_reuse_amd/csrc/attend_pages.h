@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "attend_pages_launch.h"
+#include "attend_pages_tiles.h"
 #include "hkv_device.h"
 
 namespace hkv {
@@ -143,21 +144,6 @@ __device__ __forceinline__ View view_of_wave(const Sight& v) {
   const bool any = v.hi > v.lo;
   return {wave_min(v.pre), wave_max(v.pre), wave_min(any ? v.lo : INT32_MAX), wave_max(any ? v.lo : INT32_MAX),
           wave_min(any ? v.hi : 0), wave_max(any ? v.hi : 0)};
-}
-
-// Tiles of `size` tokens that a view has: [0, pre) and [lo, hi).
-struct TileList {
-  int pre, lo, count;
-  __device__ __forceinline__ int at(int i) const { return i < pre ? i : i - pre + lo; }
-};
-
-__device__ __forceinline__ TileList tiles_of_view(int pre, int lo, int hi, int size) {
-  TileList t;
-  t.pre = (pre + size - 1) / size;
-  const int end = hi / size + (hi % size != 0);
-  t.lo = max(min(lo, hi) / size, t.pre);
-  t.count = t.pre + max(end - t.lo, 0);
-  return t;
 }
 
 // The quotient of a token and block_tokens.
