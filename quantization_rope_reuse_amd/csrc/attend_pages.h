@@ -437,13 +437,14 @@ __device__ __forceinline__ void refer_tile(f32x16 (&acc)[N], float top, RowsStat
   }
   st.scale = kPlain ? f.scale : 1.0f;
   st.shift = kOff - st.m;
-  if (kPlain && st.far) {
-    // the reference came from rounded scores: so do the weights
+  if (st.far) {
+    // The reference came from rounded scores: so do the weights.  And it is taken
+    // off by itself: beside a reference from 2^26 on kOff is lost in the shift.
 #pragma clang fp contract(off)
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[u][i] = acc[u][i] * f.scale - st.m;
+      for (int i = 0; i < 16; ++i) acc[u][i] = (kPlain ? acc[u][i] * f.scale : acc[u][i]) - st.m;
     st.scale = 1.0f;
     st.shift = kOff;
   }
