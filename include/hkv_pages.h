@@ -72,11 +72,12 @@ typedef struct {
  * over the tokens the row sees; a row that sees nothing, or whose scores are
  * all -infinity, gets out = 0 and lse = -infinity.  q, out and the pages share
  * one dtype.  Products are exact and their sums, the softmax and its sums
- * fp32 (a score beyond fp32's range is infinite, and its row's results are
- * NaN); weights enter their product rounded to the pages' type where a
- * request has many rows, and as two parts of it, 16 bits or more, where it
- * has few.  What tokens that a row does not see hold, infinities and NaN
- * included, does not reach it.  out must not overlap q.  lse: float
+ * fp32.  What leaves fp32's range is infinite: a sum of products, a score or a
+ * slope times log2(e); a row that sees a score of +infinity is NaN, and one of
+ * -infinity adds nothing.  Weights enter their product rounded to the pages'
+ * type where a request has many rows, and as two parts of it, 16 bits or more,
+ * where it has few.  What tokens that a row does not see hold, infinities and
+ * NaN included, does not reach it.  out must not overlap q.  lse: float
  * [n_tokens][n_heads], or NULL.  Rows of no request keep what out and lse
  * held.  workspace: 16-byte aligned, hkv_attend_pages_workspace_bytes() bytes
  * (0: none needed); its contents before and after do not matter, and calls

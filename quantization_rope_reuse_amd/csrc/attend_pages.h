@@ -43,7 +43,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 typedef short s8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSub = 32;                   // tokens of a subtile
-constexpr float kNoReference = -3.0e38f;
+constexpr float kNoReference = -3.4028234663852886e38f;     // the least: no score lies below it
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kFar = 0x1p16f;            // references from here on: scores are rounded before m is taken off
 

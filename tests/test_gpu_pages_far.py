@@ -1,6 +1,6 @@
 """Attention over pages whose scores are so large that fp32 holds no fraction
-of them, with a cap and with a bias as without: the token that leads takes all,
-and a row's only token gives its value.
+of them, with a cap and with a bias as without, up to the ends of fp32's range:
+the token that leads takes all, and a row's only token gives its value.
 
 Queries and keys have one element, so that the products are exact and the
 leading token is known.  Tolerances: a row's one token of any weight has its
@@ -107,3 +107,24 @@ def test_leading_token(dtype, n):
         out, lse = hkv.attend_pages(q, kp, vp, *rest, max_queries=n, sm_scale=0.0, positions=ints([50] * n),
                                     slopes=torch.full((1,), s, device=DEV))
         held(dtype, out, lse, vp, 39, -11 * float(np.float32(s)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("score", [1.9e38, 2.05e38, 2.15e38, 2.3e38])
+def test_ends_of_the_range(dtype, n, score):
+    """Scores that fp32 holds times log2(e), 3.4e38 at most: a row whose scores
+    all lie at the lower end is not an empty one."""
+    say("ends", dtype, n, score)
+    q, kp, vp, *rest = made(dtype, n, 1, [1])
+    for sign in (1, -1):
+        q.fill_(0)
+        q[:, 0, 3] = 2.0 ** 60 * sign
+        kp.fill_(0)
+        kp[0, 0, 0, 3] = 2.0 ** 40
+        out, lse = hkv.attend_pages(q, kp, vp, *rest, max_queries=n, causal=False, sm_scale=score / 2.0 ** 100)
+        held(dtype, out, lse, vp, 0, sign * score)
+    # by the bias: one token, one before the rows
+    out, lse = hkv.attend_pages(q, kp, vp, *rest, max_queries=n, sm_scale=0.0, positions=ints([1] * n),
+                                slopes=torch.full((1,), score, device=DEV))
+    held(dtype, out, lse, vp, 0, -float(np.float32(score)))
