@@ -349,6 +349,8 @@ __device__ __forceinline__ float score_of(float x, const ScoreScale& f, float di
   return s;
 }
 
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m != kNoReference; }
+
 // State of a wave's rows.
 struct RowsState {
   f32x16 o[4];
@@ -433,20 +435,25 @@ __device__ __forceinline__ void refer_tile(f32x16 (&acc)[N], float top, RowsStat
     st.l *= keep;
 #pragma unroll
     for (int d = 0; d < 4; ++d) st.o[d] *= keep;
-    st.far = __any(fabsf(m) >= kFar && m != kNoReference);
+    st.far = __any(is_far(m));
   }
   st.scale = kPlain ? f.scale : 1.0f;
   st.shift = kOff - st.m;
   if (st.far) {
-    // The reference came from rounded scores: so do the weights.  And it is taken
-    // off by itself: beside a reference from 2^26 on kOff is lost in the shift.
+    // A far reference came from rounded scores: so do the row's weights.  And it is
+    // taken off by itself: beside a reference from 2^26 on kOff is lost in the
+    // shift.  (Rows whose own reference is near keep their one rounding.)
 #pragma clang fp contract(off)
+    const bool far = is_far(st.m);
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[u][i] = (kPlain ? acc[u][i] * f.scale : acc[u][i]) - st.m;
-    st.scale = 1.0f;
-    st.shift = kOff;
+      for (int i = 0; i < 16; ++i) {
+        const float away = (kPlain ? acc[u][i] * f.scale : acc[u][i]) - st.m;
+        acc[u][i] = far ? away : acc[u][i];
+      }
+    st.scale = far ? 1.0f : st.scale;
+    st.shift = far ? kOff : st.shift;
   }
 }
 
