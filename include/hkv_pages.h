@@ -77,7 +77,8 @@ typedef struct {
  * -infinity adds nothing.  Weights enter their product rounded to the pages'
  * type where a request has many rows, and as two parts of it, 16 bits or more,
  * where it has few.  What tokens that a row does not see hold, infinities and
- * NaN included, does not reach it.  out must not overlap q.  lse: float
+ * NaN included, does not reach it (where rows meet values that are not finite,
+ * the call takes several times as long).  out must not overlap q.  lse: float
  * [n_tokens][n_heads], or NULL.  Rows of no request keep what out and lse
  * held.  workspace: 16-byte aligned, hkv_attend_pages_workspace_bytes() bytes
  * (0: none needed); its contents before and after do not matter, and calls

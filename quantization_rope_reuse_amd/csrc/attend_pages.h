@@ -23,8 +23,8 @@
 // (fp16); bf16's and fp32's range needs no offset.
 //
 // A masked token's weight is 0, but 0 times an infinite value is not: where a
-// row's sum is finite and its output is not, it is computed again, token by
-// token, over what it sees (careful_row).
+// row's sum is finite and its output is not, the wave makes its output again with
+// such values apart (output_again).
 #pragma once
 
 #include <type_traits>
@@ -543,100 +543,188 @@ struct WaveTiles {
   int first, end, step, size;
 };
 
-// The output of one row over a wave's tiles, token by token, lane i dims 2i and
-// 2i + 1: sum_m exp2(s_m - m) v_m / l over the tokens it sees with a weight
-// above 0.
-template <int DT, bool CAP, bool BIAS>
-__device__ __forceinline__ float2 careful_row(const PageAttendParams& p, const int32_t* table,
-                                                        int64_t head_off, const char* q_row, Sight v, int len,
-                                                        WaveTiles w, float m, float l, ScoreScale f) {
-  constexpr int ES = ElemSize<DT>::value;
-  const int lane = threadIdx.x & (kWave - 1);
-  auto two = [&](const char* at, float (&x)[2]) {
-    if constexpr (DT == kF32) {
-      const float2 y = reinterpret_cast<const float2*>(at)[lane];
-      x[0] = y.x;
-      x[1] = y.y;
-    } else {
-      const uint32_t y = reinterpret_cast<const uint32_t*>(at)[lane];
-      x[0] = DT == kF16 ? f16_bits_to_f32(y & 0xFFFFu) : bf16_bits_to_f32(y & 0xFFFFu);
-      x[1] = DT == kF16 ? f16_bits_to_f32(y >> 16) : bf16_bits_to_f32(y >> 16);
+// What of a type is not finite: all bits of its exponent are set.
+template <int DT>
+__device__ __forceinline__ bool not_finite(uint32_t bits) {
+  constexpr uint32_t kExponent = DT == kF32 ? 0x7F800000u : DT == kF16 ? 0x7C00u : 0x7F80u;
+  return (bits & kExponent) == kExponent;
+}
+
+// 4 consecutive elements as fp32.
+template <int DT>
+__device__ __forceinline__ f32x4 load4(const char* from) {
+  if constexpr (DT == kF32) {
+    return *reinterpret_cast<const f32x4*>(from);
+  } else {
+    const u32x2 raw = *reinterpret_cast<const u32x2*>(from);
+    f32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t bits = (raw[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+      y[i] = DT == kF16 ? f16_bits_to_f32(bits) : bf16_bits_to_f32(bits);
     }
-  };
-  static_assert(ES == 2 || ES == 4, "element sizes");
-  float q[2];
-  two(q_row, q);
-  const float sign = p.q_keep == 0 ? 0.0f : p.q_flip ? -1.0f : 1.0f;
-  float2 o = make_float2(0.0f, 0.0f);
+    return y;
+  }
+}
+
+// How far weights are made smaller where the output is made again, so that sums
+// of up to 2^31 of them (each 2^kSlack at most) times the type's largest values
+// stay in fp32's range, before the weights' sum is divided out.  (fp16's values
+// leave room; weights below 2^-126 of this lose bits, 2^-86 of a row's largest.)
+template <int DT> constexpr float kSmaller = DT == kF16 ? 1.0f : 0x1p-40f;
+
+// O^T over a wave's tiles once more, N subtiles each, for values that are not
+// finite or too large: the same products, references and weights in the same
+// order, so that a row has the same bits whatever the tokens hold that it does not
+// see, but from the pages and with every value that is not finite taken as 0.
+// Those are added by themselves to the rows where their token has a weight above 0.
+// Out of the way of the common case: no LDS, 2-byte loads and a wait at each step
+// (one token of NaN in 4,096 that all rows see: 512 queries of 32 heads take 440 us
+// for 60, a decode 30 for 18).
+template <int DT, int PP, bool CAP, bool BIAS, int N>
+__device__ __forceinline__ void output_again(const PageAttendParams& p, const int32_t* table, int64_t head_off,
+                                             const char* q_row, const Sight& v, int len, const WaveTiles& w,
+                                             const ScoreScale& f, f32x16 (&o)[4], int lane) {
+  constexpr int ES = ElemSize<DT>::value;
+  const char* none = reinterpret_cast<const char*>(kZeros);
+  const int q32 = lane & 31, h = lane >> 5;
+  Queries<DT> q;
+  q.load(q_row, h, p.q_keep, p.q_flip);
+  RowsState st;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) st.o[d] = f32x16{};
+  st.m = kNoReference;
+  st.l = 0.0f;
+  st.far = false;
   for (int i = w.first; i < w.end; i += w.step) {
     const int first = w.list.at(i) * w.size;
-    const int last = min(w.size, len - first);
-    for (int t = 0; t < last; ++t) {
-      const int token = first + t;
-      if (token >= v.pre && (token < v.lo || token >= v.hi)) continue;
-      const int block = block_of(p, token);
-      const int entry = table[block];
-      if (static_cast<uint32_t>(entry) >= static_cast<uint32_t>(p.num_pages)) continue;
-      const int64_t at = entry * p.page + (token - block * p.block_tokens) * p.token + head_off;
-      float k[2], x[2];
-      two(p.k + at, k);
-      float s = (q[0] * k[0] + q[1] * k[1]) * sign;
+    int64_t at[N];                       // places of tokens lane % 32 of the subtiles
+    uint64_t live = 0;
 #pragma unroll
-      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-      const float distance = fabsf(static_cast<float>(static_cast<double>(v.pos) - token));
-      const float weight = __builtin_amdgcn_exp2f((score_of<CAP, BIAS, false>(s, f, distance) - m) + PageTraits<DT>::kOff) / l;
-      if (weight > 0.0f) {
-        two(p.v + at, x);
-        o.x += weight * x[0];
-        o.y += weight * x[1];
+    for (int u = 0; u < N; ++u) {
+      const int token = first + kSub * u + q32;
+      const int block = block_of(p, token);
+      const int entry = token < len ? table[block] : -1;
+      const bool known = static_cast<uint32_t>(entry) < static_cast<uint32_t>(p.num_pages);
+      at[u] = known ? entry * p.page + (token - block * p.block_tokens) * p.token + head_off : int64_t{-1};
+      live |= static_cast<uint64_t>(static_cast<uint32_t>(__ballot(known))) << (kSub * u);
+    }
+    const uint64_t seen = seen_of(v, live, first, h);
+    if (!__any(seen != 0)) continue;
+    f32x16 acc[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      acc[u] = f32x16{};
+      const char* key = p.k + at[u];
+      if constexpr (DT == kF32) {
+#pragma unroll
+        for (int kk = 0; kk < 16; ++kk) {
+          const f32x4 k = *reinterpret_cast<const f32x4*>(at[u] < 0 ? none : key + (64 * h + 4 * kk) * ES);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[u] = __builtin_amdgcn_mfma_f32_32x32x2f32(k[e], q.x[kk][e], acc[u], 0, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          acc[u] = mma<DT>(*reinterpret_cast<const s8*>(at[u] < 0 ? none : key + (16 * kk + 8 * h) * ES), q.x[kk], acc[u]);
+      }
+    }
+    const float from_first = BIAS ? static_cast<float>(static_cast<double>(v.pos) - (first + 4 * h)) : 0.0f;
+    const float top = scores_of<CAP, BIAS, N>(acc, f, from_first);
+    refer_tile<DT, CAP, BIAS, N>(acc, top, st, f, true, seen);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float weight[16], smaller[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        weight[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u][e], st.scale, st.shift));
+        smaller[e] = weight[e] * kSmaller<DT>;
+      }
+      Weights<DT, PP> operand;
+      operand.set(smaller);
+      uint32_t odd = 0;                  // tokens with a value that is not finite
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {      // (halves by themselves: fewer registers)
+        __builtin_amdgcn_sched_barrier(0);
+        s8 x[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int t = 16 * s + 8 * (e >> 2) + (e & 3);
+          const int64_t place = __shfl(at[u], t + 4 * h);
+          const char* value = place < 0 ? none : p.v + place + q32 * ES;
+          const int step = place < 0 ? 0 : 32 * ES;
+          bool bad = false;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            if constexpr (DT == kF32) {
+              const uint32_t bits = *reinterpret_cast<const uint32_t*>(value + d * step);
+              const bool is = not_finite<DT>(bits);
+              bad = bad || is;
+              st.o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(is ? 0.0f : __builtin_bit_cast(float, bits),
+                                                             operand.w[8 * s + e], st.o[d], 0, 0, 0);
+            } else {
+              const uint16_t bits = *reinterpret_cast<const uint16_t*>(value + d * step);
+              const bool is = not_finite<DT>(bits);
+              bad = bad || is;
+              x[d][e] = is ? 0 : static_cast<short>(bits);
+            }
+          }
+          const uint64_t all = __ballot(bad);
+          odd |= static_cast<uint32_t>(static_cast<uint32_t>(all) != 0) << t |
+                 static_cast<uint32_t>((all >> 32) != 0) << (t + 4);
+        }
+        if constexpr (DT != kF32) {
+#pragma unroll
+          for (int pp = PP - 1; pp >= 0; --pp)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) st.o[d] = mma<DT>(x[d], operand.part[pp][s], st.o[d]);
+        }
+      }
+      while (odd) {
+        const int t = __builtin_ctz(odd);
+        odd &= odd - 1;
+        float mine = 0.0f;               // token t's weight, in the lanes that have it
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mine = 8 * (e >> 2) + (e & 3) == (t & ~4) ? weight[e] : mine;
+        const float that = __shfl(mine, q32 + 8 * (t & 4));
+        const char* value = p.v + __shfl(at[u], t) + 4 * h * ES;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const f32x4 y = load4<DT>(value + (32 * d + 8 * a) * ES);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              st.o[d][4 * a + b] += that > 0.0f && !(fabsf(y[b]) < INFINITY) ? that * y[b] : 0.0f;
+          }
       }
     }
   }
-  return o;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = st.o[d];
 }
 
-// Divides the sum out (l becomes the row's whole sum of this wave's tokens) and
-// computes again the rows that a masked token's value has spoilt.
-template <int DT, bool CAP, bool BIAS>
+// Divides the sum out (l becomes the row's whole sum of this wave's tokens), of
+// an output that is made again where some row's is not finite.
+template <int DT, int PP, bool CAP, bool BIAS, int N>
 __device__ __forceinline__ void finish_rows(const PageAttendParams& p, const int32_t* table, int64_t head_off,
                                             const char* q_row, const Sight& v, int len, const WaveTiles& w,
                                             RowsState& st, const ScoreScale& f, int lane) {
   st.l += __shfl_xor(st.l, 32);
-  const float inv = 1.0f / st.l;
+  float inv = 1.0f / st.l;
   bool bad = false;
 #pragma unroll
   for (int d = 0; d < 4; ++d)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float y = st.l == 0.0f ? 0.0f : st.o[d][i] * inv;
-      st.o[d][i] = y;
-      bad = bad || !(fabsf(y) < INFINITY);
-    }
-  bad = bad && st.l < INFINITY;
-  uint64_t rows = __ballot(bad);
-  rows = (rows | (rows >> 32)) & 0xFFFFFFFFu;
-  while (rows) {
-    const int c = __builtin_ctzll(rows);
-    rows &= rows - 1;
-    const uint64_t at = reinterpret_cast<uint64_t>(q_row);
-    const uint64_t row = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(at >> 32), c)) << 32 |
-                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(at), c));
-    const Sight sight = {__builtin_amdgcn_readlane(v.pre, c), __builtin_amdgcn_readlane(v.lo, c),
-                         __builtin_amdgcn_readlane(v.hi, c), __builtin_amdgcn_readlane(v.pos, c)};
-    const ScoreScale g = {f.scale, f.top, __shfl(f.slope, c)};
-    const float2 y = careful_row<DT, CAP, BIAS>(p, table, head_off, reinterpret_cast<const char*>(row), sight, len, w,
-                                                __shfl(st.m, c), __shfl(st.l, c), g);
-    const int h = lane >> 5;
-    const bool mine = (lane & 31) == c;
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        // dim 32 d + 8 (i / 4) + 4 h + i % 4
-        const float x = __shfl(i & 1 ? y.y : y.x, 16 * d + 4 * (i >> 2) + 2 * h + ((i & 3) >> 1));
-        st.o[d][i] = mine ? x : st.o[d][i];
-      }
+    for (int i = 0; i < 16; ++i) bad = bad || !(fabsf(st.o[d][i] * inv) < INFINITY);
+  if (__any(bad && st.l > 0.0f && st.l < INFINITY)) {
+    output_again<DT, PP, CAP, BIAS, N>(p, table, head_off, q_row, v, len, w, f, st.o, lane);
+    inv *= 1.0f / kSmaller<DT>;
   }
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st.o[d][i] = st.l == 0.0f ? 0.0f : st.o[d][i] * inv;
   st.l *= __builtin_amdgcn_exp2f(-PageTraits<DT>::kOff);
 }
 

@@ -314,7 +314,7 @@ void page_chunk_kernel(PageAttendParams p) {
       }
     }
     const WaveTiles mine = {list, t0, t1, 1, kTile};
-    finish_rows<DT, CAP, BIAS>(p, table, head_off, q_row, sight, s.len, mine, st, f, lane);
+    finish_rows<DT, 1, CAP, BIAS, N>(p, table, head_off, q_row, sight, s.len, mine, st, f, lane);
 
     const int id = here(lane), last_h = id >> 5;
     const int last_row = row0 + kItemRows * wave + (id & 31);

@@ -285,7 +285,7 @@ void page_rows_kernel(PageAttendParams p) {
       while (i < seg1) step(keys, values);
     }
     const WaveTiles mine = {list, seg0 + wave, seg1, kPageRowsWaves, kPageRowsTile};
-    finish_rows<DT, CAP, BIAS>(p, table, head_off, q_row, sight, s.len, mine, st, f, lane);
+    finish_rows<DT, PP, CAP, BIAS, 1>(p, table, head_off, q_row, sight, s.len, mine, st, f, lane);
 
     // The waves join: wave d takes dims 32 d ..
     const int last_lane = here(lane), last_q = last_lane & 31, last_h = last_lane >> 5;
