@@ -18,7 +18,7 @@ import torch
 
 from parity_util import TORCH_OF, host_f64
 from quantization_rope_reuse_amd import hkv
-from test_gpu_pages import DEV, HALF, TINY, dev, ints, say
+from test_gpu_pages import DEV, HALF, TINY, check, dev, ints, say, setup
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,18 @@ def test_ends_of_the_range(dtype, n, score):
     out, lse = hkv.attend_pages(q, kp, vp, *rest, max_queries=n, sm_scale=0.0, positions=ints([1] * n),
                                 slopes=torch.full((1,), score, device=DEV))
     held(dtype, out, lse, vp, 0, -float(np.float32(score)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n", [4, 70])
+def test_positions_near_the_largest(dtype, n):
+    """Rows at positions up to 2^31 - 1 that see a prefix, or all of it, with a
+    bias by their distance: against the oracle, as in test_gpu_pages.py."""
+    say("far positions", dtype, n)
+    case = (dtype, 16, 2, 4, [200, 90], [n, n // 2], "tokens")
+    g, kp, vp, table, q_start, q = setup(case, 51)
+    positions = 2 ** 31 - 1 - g.integers(0, 300, q.shape[0])
+    for slope in (1e-7, 1e-6, -1e-6):
+        for kw in (dict(window=40, prefix_len=[150, 33]), dict(), dict(causal=False, cap=20.0)):
+            check(q, kp, vp, table, [200, 90], q_start, "far positions", n == 70, max_queries=n, positions=positions,
+                  slopes=np.full(8, slope), **kw)

@@ -9,8 +9,11 @@ import numpy as np
 import pytest
 import torch
 
+from attend_pages_paths import CASES, ident
+from oracle import pages_oracle as P
 from parity_util import TORCH_OF, host_f64
 from quantization_rope_reuse_amd import hkv
+from test_gpu_attend_pages_paths import made as paths_made
 from test_gpu_pages import DEV, dev, fresh, ints, say
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +123,34 @@ def test_values_near_the_largest(dtype, n):
     # weights of 8, 16 or 24 bits against their sum, 300 sums in fp32, the result's rounding
     want = host_f64((torch.ones((), device=DEV) * big).to(TORCH_OF[dtype]))
     assert (np.abs(host_f64(out) / want - 1) <= 2 * half + 2.0 ** -8 * (dtype == "bf16") + 300 * 2.0 ** -24 + 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("case", CASES, ids=ident)
+def test_unseen_by_every_way_of_sharing_out(case):
+    """Ranges, cuts and joins, with entries left out: some of each request's tokens
+    not finite, rows that see none of them."""
+    say("unseen, shared out", case)
+    dtype, tb, h, group, lens, asks, own, share = case
+    g, kp, vp, table, q_start, q, kw, _ = paths_made(case, 34)
+    n = q.shape[0]
+    window = max(lens) // 20
+    positions = np.concatenate([np.sort(g.integers(0, max(x, 1), a)) for x, a in zip(lens, asks)]).astype(np.int64)
+    kb, vb = kp.clone(), vp.clone()
+    fine = np.ones(n, bool)
+    for r, x in enumerate(lens):
+        held = -(-x // tb)
+        table[r, :held][g.random(held) < 0.1] = -1
+        bad = np.unique(g.integers(0, x, 1 + x // 300)) if x else np.zeros(0, np.int64)
+        for i in range(q_start[r], q_start[r + 1]):
+            fine[i] = not P.sight(x, 0, 0, positions[i], 0, 2, window)[bad].any()
+        for t in bad:
+            page = int(table[r, t // tb])
+            if page >= 0:
+                vb[page, t % tb], kb[page, t % tb] = float("nan"), float("inf")
+    fine = dev(fine)
+    args = (ints(np.minimum(table, 2 ** 30)), ints(lens), ints(q_start))
+    more = dict(max_queries=max(asks), positions=ints(positions), window=window, prefix_len=ints([2] * len(lens)))
+    clean, cl = hkv.attend_pages(q, kp, vp, *args, **more)
+    out, lse = hkv.attend_pages(q, kb, vb, *args, **more)
+    assert torch.equal(out[fine], clean[fine]) and torch.equal(lse[fine], cl[fine])
+    assert torch.isfinite(clean.float()).all()
