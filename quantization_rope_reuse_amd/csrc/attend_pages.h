@@ -589,7 +589,9 @@ __device__ __forceinline__ void output_again(const PageAttendParams& p, const in
   const char* none = reinterpret_cast<const char*>(kZeros);
   const int q32 = lane & 31, h = lane >> 5;
   Queries<DT> q;
-  q.load(q_row, h, p.q_keep, p.q_flip);
+  // (as scalars of their own: loaded together with their neighbours they put those
+  // parameters into scratch memory for the whole kernel)
+  q.load(q_row, h, __builtin_amdgcn_readfirstlane(p.q_keep), __builtin_amdgcn_readfirstlane(p.q_flip));
   RowsState st;
 #pragma unroll
   for (int d = 0; d < 4; ++d) st.o[d] = f32x16{};
