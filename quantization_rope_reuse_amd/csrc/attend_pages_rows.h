@@ -170,7 +170,10 @@ void page_rows_kernel(PageAttendParams p) {
       while (before(r + 1) <= at) ++r;
     r = __builtin_amdgcn_readfirstlane(r);
     const PageSpan s = page_span(p, r);
-    const TileList list = dealt_tiles(p, s);
+    TileList list = dealt_tiles(p, s);     // (the same in all lanes: branches on it are scalar)
+    list.pre = __builtin_amdgcn_readfirstlane(list.pre);
+    list.lo = __builtin_amdgcn_readfirstlane(list.lo);
+    list.count = __builtin_amdgcn_readfirstlane(list.count);
     int seg0 = 0, seg1 = list.count, dealt = 0;
     bool whole = true;
     if (p.ranges > 0) {
