@@ -74,9 +74,12 @@ typedef struct {
  * one dtype.  Products are exact and their sums, the softmax and its sums
  * fp32.  What leaves fp32's range is infinite: a sum of products, a score or a
  * slope times log2(e); a row that sees a score of +infinity is NaN, and one of
- * -infinity adds nothing.  Weights enter their product rounded to the pages'
- * type where a request has many rows, and as two parts of it, 16 bits or more,
- * where it has few.  What tokens that a row does not see hold, infinities and
+ * -infinity adds nothing.  Weights of 16-bit types enter their product as two
+ * parts of the type, 16 bits or more, where the call's requests have fewer than
+ * 64 rows of a key head each on average or the call is small, and rounded to the
+ * type (8 bits, 11 in fp16) where they have more: one kernel takes the whole
+ * call.  So decodes beside a long prompt are better given a call of their own,
+ * for their precision and their time.  What tokens that a row does not see hold, infinities and
  * NaN included, does not reach it (where rows meet values that are not finite,
  * the call takes several times as long).  out must not overlap q.  lse: float
  * [n_tokens][n_heads], or NULL.  Rows of no request keep what out and lse

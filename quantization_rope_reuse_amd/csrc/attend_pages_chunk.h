@@ -5,17 +5,23 @@
 // tokens that some of them see in tiles of 64 (fp32: 32), which each wave brings a
 // quarter of into LDS and uses whole for its own rows; one barrier a tile, behind
 // which the tile after next sets out.  Two workgroups fit a CU (80 KB of LDS, 256
-// registers a lane), so that one's barriers, first loads and last stores hide
-// behind the other's products.
+// registers a lane; the 16-bit kernels spill none of them, those of fp32 three), so
+// that one's barriers, first loads and last stores hide behind the other's products.
 //
 // Bound by issue: a wave's matrix instructions take 14 ns each, and of the vector
 // work beside them (an exponential, a fused product, half a conversion, a sum and
 // half a maximum a score) only about half hides behind them; a wave alone on its
 // SIMD leaves the rest idle.  2,048 queries over 16,384 tokens (32 heads, 515
-// GFLOP) take 524 us, 0.98 PFLOP/s, where the same products by the library's
-// largest matrix product would take 410; 64 rows a wave with one wave a SIMD 780,
-// 8 waves sharing a tile (half the loads into LDS, one workgroup a CU) 540, but
-// 179 for 158 with prompts of documents, whose items are short.
+// GFLOP) take 528 to 546 us, 0.94 to 0.98 PFLOP/s, where the same products by the
+// library's largest matrix product would take 410; 64 rows a wave with one wave a
+// SIMD 780, 8 waves sharing a tile (half the loads into LDS, one workgroup a CU) 540
+// where this took 524, and 179 for 158 with prompts of documents, whose items are
+// short.
+//
+// Weights enter the second product rounded to the pages' type (2^-8 of each at most
+// in bf16, 2^-11 in fp16): a second part of them would make half of the matrix work
+// twice as long.  Against 64 bits a result's error is 1.4 times that of rounding it
+// alone.
 #pragma once
 
 #include <type_traits>

@@ -8,12 +8,17 @@
 //
 // Keys and values come straight into LDS, one tile of each per wave: the next
 // tile's keys set out as soon as the scores are made, its values behind the
-// output, so that one or both are always under way and no wave waits for
-// another.  Memory bounds it (fp32: the matrix instructions): loads of random
+// output, and no wave waits for another.  The waits set by hand let the one be under
+// way beside the other.  The compiler's do not: it waits for all of a wave's loads
+// before it uses a table entry that an earlier turn has loaded (so the next keys set
+// out behind this tile's values) and before it loads the next one into the same
+// register (so the next values set out behind the next keys).  What overlaps is the
+// four waves.  Memory bounds it (fp32: the matrix instructions): loads of random
 // 64-token pages into LDS reach 5.7 TB/s on this card; 32 requests of up to 8,192
-// tokens (64 heads over 8, bf16, 473 MB) take 95 to 109 us, 4.3 to 5.0 TB/s, one of
-// 65,519 54 (5.0), the rest setting out, and passing from a request to the next.
-// Two workgroups a CU take 127, table entries read for groups of tokens 124.
+// tokens (64 heads over 8, bf16, 473 MB) take 96 to 108 us, 4.4 to 4.9 TB/s, one of
+// 65,519 53 (5.1), the rest those waits, setting out, and passing from a request to
+// the next.  With two workgroups a CU the first take 117 us for 110, both with the
+// join.
 #pragma once
 
 #include "attend_pages.h"
@@ -257,7 +262,7 @@ void page_rows_kernel(PageAttendParams p) {
         const uint32_t live = live_next;
         const int first = list.at(i) * kPageRowsTile;
         int after = seg1;
-        wait_loads<kLoads>();              // the keys; the values may be under way
+        wait_loads<kLoads>();              // the keys; the values need not be there
         f32x16 acc[1] = {score_tile<DT>(k_area, q, lane)};
         wait_loads<kLoads>();              // the keys are read
         if (next < seg1) {
@@ -273,7 +278,7 @@ void page_rows_kernel(PageAttendParams p) {
         refer_tile<DT, CAP, BIAS, 1>(acc, scores_of<CAP, BIAS, 1>(acc, f, from_first), st, f, part, seen);
         st.l += weigh_tile<DT, PP>(acc[0], w[0], st);
         if (next < seg1)
-          wait_loads<kLoads>();            // the values; the next keys may be under way
+          wait_loads<kLoads>();            // the values; the next keys need not be there
         else
           wait_loads<0>();
         output_tile<DT, PP>(v_area, w[0], st.o, lane);

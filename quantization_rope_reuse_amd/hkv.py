@@ -956,7 +956,9 @@ def attend_pages(q, k_pages, v_pages, block_table, kv_len, q_start=None, max_que
     document) on that lie up to it (causal) and less than `window` before it.
     cap: scores become cap * tanh(score / cap); slopes (float32 [n_q_heads]):
     the head's slope times the distance is taken off.  sm_scale: 1 / sqrt(128)
-    if None."""
+    if None.  One kernel takes the whole call, chosen by sizes: decodes beside a
+    long prompt are faster, and more precise in 16-bit types, in a call of their
+    own, and a close max_queries (with q_start n_tokens if None) is worth giving."""
     st, out, lse = native().attend_pages(
         q, k_pages, v_pages, block_table, kv_len, q_start,
         -1 if max_queries is None else max(int(max_queries), 0),
